@@ -334,6 +334,139 @@ size_t pivot_workspace_size(int32_t mode, int32_t dtype, int32_t L_or_maxlen, in
 pivot_status_t pivot_decode_noalloc(const pivot_decode_t* batch, int32_t mode, int32_t C,
                                     int32_t topk, int32_t* idx, int32_t* cand, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The paged key/value cache that the selected positions index, and the
+ * attention that reads it.
+ * ------------------------------------------------------------------------ */
+
+/* Keys and values of B sequences on pages of page_size tokens.  Token t of
+ * sequence b sits in slot t % page_size of page table[b][t / page_size].
+ * PIVOT_E4M3 planes hold codes with one float32 scale per token for K and
+ * one for V (value = code * scale).  len[b] counts the sequence's tokens;
+ * table entries past its pages are -1; refs[p] counts the table entries
+ * that name page p, and a page with refs 0 is free.  A program starts with
+ * table -1, len 0 and refs 0 and lets the calls below keep them; the calls
+ * read and write all three on the device, in stream order, so a whole step
+ * can be captured into a graph and replayed.
+ *   page_size 16, 32, 64, 128 or 256; num_pages * page_size < 2^31;
+ *   1 <= B <= 65536; D * (bytes of a value) a multiple of 16 (attention:
+ *   D = 64 or 128); k, v 16-byte aligned.
+ * What the host cannot check sets the error word (PIVOT_ERR_DEVICE).  Row
+ * offsets, sequence ids, counts or lengths out of range: the append and the
+ * page calls then change nothing, and attention leaves the rows of that
+ * sequence unwritten.  A page id out of range: the append changes nothing,
+ * the other page calls pass over that table entry, and attention counts the
+ * page's tokens as masked. */
+typedef struct {
+    int32_t dtype;               /* PIVOT_BF16 or PIVOT_E4M3                     */
+    int32_t B, Hkv, D;           /* sequences, key/value heads, head dim         */
+    int32_t page_size, num_pages;
+    int32_t max_pages;           /* columns of the table                         */
+    void* k;                     /* [num_pages, page_size, Hkv, D]               */
+    void* v;
+    float* k_scale;              /* [num_pages, page_size] for PIVOT_E4M3        */
+    float* v_scale;
+    int32_t* table;              /* [B, max_pages]                               */
+    int32_t* len;                /* [B]                                          */
+    int32_t* refs;               /* [num_pages]                                  */
+} pivot_cache_t;
+
+/* Appends new tokens: rows [cu_new[b], cu_new[b+1]) of k_new and v_new
+ * (bf16 [total, Hkv, D], 16-byte aligned) become the tokens from len[b] on
+ * of sequence b, and len[b] grows by their count (which may be 0, and is at
+ * most max_new).  cu_new [B + 1] is on the device; rows from cu_new[B] on
+ * are not read.  Pages are taken lowest free id first, sequence after
+ * sequence.  A sequence whose last page is partly filled and shared
+ * (refs > 1 when the call begins) first gets a page of its own with that
+ * page's tokens copied, so no other sequence sees the new tokens.
+ * PIVOT_E4M3: a token's scale is its largest |value| over heads and dims
+ * / 448 (1 where that is 0), codes round to nearest even, saturating.
+ * lack [1] receives 0, or the number of free pages missing: then nothing
+ * has changed.  A sequence that would outgrow its table row is an error of
+ * the data (lack -1, nothing changed).  ws: 256-byte aligned. */
+pivot_status_t pivot_cache_append(const pivot_cache_t* cache, const void* k_new,
+                                  const void* v_new, const int32_t* cu_new, int32_t total,
+                                  int32_t max_new, int32_t* lack, void* ws, size_t ws_bytes,
+                                  void* stream);
+size_t pivot_cache_append_workspace_size(const pivot_cache_t* cache, int32_t total);
+
+/* Makes sequence dst[i] a copy of sequence src[i] as it stood before the
+ * call, for i < n (device arrays): its table row and length, the pages
+ * shared (their refs grow; the pages dst[i] held before lose one).  A
+ * sequence may be the source of many and a destination itself (beam
+ * reordering); the destinations are distinct.  ws: 256-byte aligned. */
+pivot_status_t pivot_pages_fork(const pivot_cache_t* cache, const int32_t* src,
+                                const int32_t* dst, int32_t n, void* ws, size_t ws_bytes,
+                                void* stream);
+size_t pivot_pages_fork_workspace_size(const pivot_cache_t* cache, int32_t n);
+
+/* Cuts sequence seqs[i] to its first keep[i] tokens (0 frees it; a keep past
+ * its length changes nothing), for i < n (device arrays, seqs distinct):
+ * pages behind the kept tokens leave its table row and lose one reference. */
+pivot_status_t pivot_pages_free(const pivot_cache_t* cache, const int32_t* seqs,
+                                const int32_t* keep, int32_t n, void* stream);
+
+/* Copies page src_ids[i] of one plane to page dst_ids[i] of another (or the
+ * same), for i < n (device arrays): page_bytes bytes each, a multiple of
+ * 16, both planes 16-byte aligned, src_pages / dst_pages pages long.  No
+ * destination is named twice or is also a source in the same plane.  An id
+ * out of range sets the error word and that copy is left out.  Any array of
+ * equal rows is a plane: copying rows of the indexer's key cache kc, pages
+ * of maxlen * D codes, keeps it in step with a fork. */
+pivot_status_t pivot_pages_copy(const void* src, int32_t src_pages, void* dst,
+                                int32_t dst_pages, size_t page_bytes, const int32_t* src_ids,
+                                const int32_t* dst_ids, int32_t n, void* stream);
+
+/* Moves the pages in use to the lowest ids: with U pages in use, the i-th
+ * used id >= U moves to the i-th free id < U (both ascending); K, V, scales,
+ * refs and table follow, and ids from U on are free.  remap [num_pages]
+ * receives every used page's new id (-1: it was free), used [1] receives U;
+ * either may be NULL.  ws: 256-byte aligned. */
+pivot_status_t pivot_pages_compact(const pivot_cache_t* cache, int32_t* remap, int32_t* used,
+                                   void* ws, size_t ws_bytes, void* stream);
+size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
+
+/* Attention of new tokens, whose keys and values are in the cache already:
+ * row i of sequence b (0 <= i < n_b = cu_new[b+1] - cu_new[b] <= max_new)
+ * is its token at position p = len[b] - n_b + i.  Head h reads key/value
+ * head h / (Hq / Hkv):
+ *     s_t = scale * q . k_t,   o = sum_t e^(s_t) v_t / sum_t e^(s_t),
+ *     lse = log sum_t e^(s_t)
+ * over its positions t; with none, o = 0 and lse = -inf.
+ * pivot_paged_attention: t in (p - window, p], or [0, p] for window 0.
+ * Table entries of pages that lie before every new token's window may be
+ * -1.
+ * pivot_selected_attention: t over row cu_new[b] + i of idx, entries outside
+ * [0, p] (-1 padding) left out; an entry named twice counts twice.  idx rows
+ * are what the indexer's calls write, in either order.
+ * Slots past a sequence's tokens may hold anything; the tokens' own stored
+ * keys and values are finite.  Rows of o and lse from cu_new[B] on stay as
+ * they were.  Products of bf16 keys and values run on the tensor cores with
+ * fp32 sums; softmax statistics and sums are fp32; weights are rounded to
+ * bf16 for the product with V.  scale: any positive finite value. */
+typedef struct {
+    int32_t Hq;                  /* query heads, a multiple of Hkv               */
+    int32_t total;               /* rows of q                                    */
+    int32_t max_new;             /* at least every sequence's count              */
+    const void* q;               /* bf16 [total, Hq, D], 16-byte aligned         */
+    const int32_t* cu_new;       /* [B + 1] on the device                        */
+    float scale;
+    int32_t window;              /* 0: the whole prefix (selected: must be 0)    */
+    const int32_t* idx;          /* [total, topk] (paged: NULL)                  */
+    int32_t topk;                /* 1 .. 65536 (paged: 0)                        */
+    void* o;                     /* bf16 [total, Hq, D], 16-byte aligned         */
+    float* lse;                  /* [total, Hq] or NULL                          */
+} pivot_attend_t;
+
+pivot_status_t pivot_paged_attention(const pivot_cache_t* cache, const pivot_attend_t* call,
+                                     void* ws, size_t ws_bytes, void* stream);
+size_t pivot_paged_attention_workspace_size(const pivot_cache_t* cache,
+                                            const pivot_attend_t* call);
+pivot_status_t pivot_selected_attention(const pivot_cache_t* cache, const pivot_attend_t* call,
+                                        void* ws, size_t ws_bytes, void* stream);
+size_t pivot_selected_attention_workspace_size(const pivot_cache_t* cache,
+                                               const pivot_attend_t* call);
+
 /* Waits for `stream`, then returns and clears the current device's error
  * word: PIVOT_OK, PIVOT_ERR_TIMEOUT or PIVOT_ERR_DEVICE (PIVOT_ERR_CUDA if
  * the wait itself failed). */

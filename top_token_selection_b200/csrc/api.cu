@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "profile.h"
 
@@ -1855,5 +1856,9 @@ pivot_status_t decode_check_args(const pivot_decode_t* b, int32_t mode, int32_t 
     if (topk > MAX_K || C > MAX_K) return PIVOT_ERR_UNSUPPORTED;
     return PIVOT_OK;
 }
+
+pivot_status_t status_of(cudaError_t e) { return from_cuda(e); }
+int sm_count() { return num_sms(); }
+TensorMapEncodeFn tensor_map_encode() { return encode_fn(); }
 
 }  // namespace pivot

@@ -1,0 +1,153 @@
+// attend.h -- attention over the paged cache: parameters and launchers.
+#pragma once
+
+#include "paged.cuh"
+
+namespace pivot {
+
+// Work is counted in units of one key tile for one block of query rows and
+// one key/value head.  The units of a call are numbered sequence by
+// sequence, head by head, row block by row block, and CTA c of n takes the
+// contiguous run [c U / n, (c + 1) U / n): every CTA gets the same work
+// whatever the lengths.  A row block ("item") that more than one CTA worked
+// on leaves partial sums in the workspace, which a second kernel joins.
+//
+// The query rows of a sequence for one key/value head are its new tokens'
+// heads of that group, token by token: row r is token r / G, head r % G.
+struct AttendParams {
+    CacheView c;
+    const uint16_t* q;          // bf16 [total, Hq, D]
+    const int32_t* cu;          // [B + 1]
+    const int32_t* idx;         // [total, topk] or NULL
+    uint16_t* o;
+    float* lse;
+    int Hq, G, total, max_new, window, topk;
+    float scale_log2;           // scale * log2(e)
+    int R, TK;                  // rows of a block, keys of a tile
+    // plan of a paged call (the selected call's is arithmetic)
+    long long* seq_units;       // [B + 1] units before sequence b
+    int32_t* blk_off;           // [B + 1] row blocks before sequence b
+    long long* blk_units;       // per row block: tiles of its sequence's blocks up to it
+    // partial sums: slots 2c (a CTA's item that began before its run) and
+    // 2c + 1 (one that it began): R rows of D sums, then R maxima, R sums
+    float* part;
+    int ncta;
+};
+
+// One item and where it lies among the units.
+struct Item {
+    int b, h;                   // sequence, key/value head
+    int row0, rows;             // its query rows (of the sequence's n G)
+    int first;                  // packed row of the sequence's first new token
+    int pos0;                   // position of that token
+    int tile0, tiles;           // key tiles
+    long long unit0;            // first unit
+    bool ok;
+};
+
+// Total units of the call.
+__device__ __forceinline__ int blocks_per_token(const AttendParams& p) { return (p.G + p.R - 1) / p.R; }
+__device__ __forceinline__ int selected_tiles(const AttendParams& p) { return (p.topk + p.TK - 1) / p.TK; }
+
+template <bool SELECTED>
+__device__ __forceinline__ long long total_units(const AttendParams& p) {
+    if constexpr (SELECTED) {
+        int rows = p.cu[p.c.B];
+        if (rows < 0 || rows > p.total) {
+            raise_error(ERRBIT_DATA);
+            rows = 0;
+        }
+        return (long long)rows * p.c.Hkv * blocks_per_token(p) * selected_tiles(p);
+    } else {
+        return p.seq_units[p.c.B];
+    }
+}
+
+// First unit of CTA c's run.
+__device__ __forceinline__ long long run_begin(long long units, int c, int ncta) {
+    return units * c / ncta;
+}
+// The CTA whose run holds unit u.
+__device__ __forceinline__ int run_of(long long units, long long u, int ncta) {
+    return (int)(((u + 1) * ncta - 1) / units);
+}
+
+// Row blocks and tiles of a paged call's sequence.
+__device__ __forceinline__ void block_tiles(const AttendParams& p, int pos0, int row0, int rows,
+                                            int& tile0, int& tiles) {
+    const int hi = pos0 + (row0 + rows - 1) / p.G;               // the last token's position
+    const int lo = p.window ? max(0, pos0 + row0 / p.G - p.window + 1) : 0;
+    tile0 = lo / p.TK;
+    tiles = hi / p.TK + 1 - tile0;
+}
+
+template <bool SELECTED>
+__device__ __forceinline__ Item find_item(const AttendParams& p, long long u) {
+    Item it;
+    it.ok = true;
+    if constexpr (SELECTED) {
+        const int nt = selected_tiles(p), nb = blocks_per_token(p);
+        long long i = u / nt;
+        it.unit0 = i * nt;
+        const int blk = (int)(i % nb);
+        i /= nb;
+        it.h = (int)(i % p.c.Hkv);
+        const int r = (int)(i / p.c.Hkv);
+        it.b = seq_of_row(p.cu, p.c.B, r);
+        int first = 0, n = 0, len = 0;
+        it.ok = new_rows(p.c, p.cu, it.b, p.total, p.max_new, first, n, len);
+        if (it.ok && len < n) {
+            raise_error(ERRBIT_DATA);
+            it.ok = false;
+        }
+        if (it.ok && (r < first || r >= first + n)) it.ok = false;   // before the first offset
+        it.first = r;
+        it.pos0 = len - n + r - first;
+        it.row0 = blk * p.R;
+        it.rows = min(p.R, p.G - it.row0);
+        it.tile0 = 0;
+        it.tiles = nt;
+    } else {
+        int lo = 0, hi = p.c.B - 1;
+        while (lo < hi) {                        // last b with seq_units[b] <= u
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.seq_units[mid] <= u) lo = mid; else hi = mid - 1;
+        }
+        it.b = lo;
+        const int blk0 = p.blk_off[lo], nblk = p.blk_off[lo + 1] - blk0;
+        const long long* cum = p.blk_units + blk0;
+        const long long per_head = cum[nblk - 1];
+        const long long in_seq = u - p.seq_units[lo];
+        it.h = (int)(in_seq / per_head);
+        const long long in_head = in_seq % per_head;
+        int a = 0, z = nblk - 1;
+        while (a < z) {                          // first block whose units end after in_head
+            const int mid = (a + z) >> 1;
+            if (cum[mid] > in_head) z = mid; else a = mid + 1;
+        }
+        it.unit0 = p.seq_units[lo] + it.h * per_head + (a ? cum[a - 1] : 0);
+        it.first = p.cu[lo];
+        const int n = p.cu[lo + 1] - it.first;
+        it.pos0 = p.c.len[lo] - n;
+        it.row0 = a * p.R;
+        it.rows = min(p.R, n * p.G - it.row0);
+        block_tiles(p, it.pos0, it.row0, it.rows, it.tile0, it.tiles);
+    }
+    return it;
+}
+
+__device__ __forceinline__ size_t slot_words(int R, int D) { return (size_t)R * (D + 2); }
+
+// Bytes of the plan and of the partial sums.
+size_t attend_plan_bytes(int B, int total, int G, int R);
+size_t attend_part_bytes(int ncta, int R, int D);
+
+cudaError_t launch_attend_plan(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_rows(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t st);
+
+// CTAs and tile of the rows kernel.
+constexpr int ROWS_CTAS_PER_SM = 2;
+inline int rows_tile(int dtype) { return dtype == PIVOT_E4M3 ? 128 : 64; }
+
+}  // namespace pivot

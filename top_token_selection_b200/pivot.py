@@ -36,7 +36,12 @@ ABI_SYMBOLS = [
     "pivot_index_varlen_workspace_size", "pivot_index_window_outside",
     "pivot_index_window_outside_workspace_size", "pivot_set_score_buffer_cap",
     "pivot_workspace_size", "pivot_set_fused_selection", "pivot_refine_adaptive",
-    "pivot_refine_adaptive_workspace_size",
+    "pivot_refine_adaptive_workspace_size", "pivot_cache_append",
+    "pivot_cache_append_workspace_size", "pivot_pages_fork", "pivot_pages_fork_workspace_size",
+    "pivot_pages_free", "pivot_pages_copy", "pivot_pages_compact",
+    "pivot_pages_compact_workspace_size", "pivot_paged_attention",
+    "pivot_paged_attention_workspace_size", "pivot_selected_attention",
+    "pivot_selected_attention_workspace_size",
 ]
 KERNELS = {0: "scan", 1: "select", 2: "refine", 3: "reduce", 4: "reuse"}
 
@@ -68,6 +73,22 @@ class PivotDecode(ctypes.Structure):
                 ("q", ctypes.c_void_p), ("q_scale", ctypes.c_void_p), ("w", ctypes.c_void_p),
                 ("kc", ctypes.c_void_p), ("kc_scale", ctypes.c_void_p),
                 ("cache_len", ctypes.c_void_p), ("order", ctypes.c_int32)]
+
+
+class PivotCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("refs", ctypes.c_void_p)]
+
+
+class PivotAttend(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("total", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("cu_new", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int32), ("idx", ctypes.c_void_p), ("topk", ctypes.c_int32),
+                ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
 _lib = None
@@ -116,6 +137,18 @@ def load(path: str = LIB_PATH):
         "pivot_refine_adaptive": ([P, I32, P, P, I32, I32, ctypes.c_float, P, P, P, P, SZ, P],
                                   I32),
         "pivot_refine_adaptive_workspace_size": ([P, I32, I32, I32], SZ),
+        "pivot_cache_append": ([P, P, P, P, I32, I32, P, P, SZ, P], I32),
+        "pivot_cache_append_workspace_size": ([P, I32], SZ),
+        "pivot_pages_fork": ([P, P, P, I32, P, SZ, P], I32),
+        "pivot_pages_fork_workspace_size": ([P, I32], SZ),
+        "pivot_pages_free": ([P, P, P, I32, P], I32),
+        "pivot_pages_copy": ([P, I32, P, I32, SZ, P, P, I32, P], I32),
+        "pivot_pages_compact": ([P, P, P, P, SZ, P], I32),
+        "pivot_pages_compact_workspace_size": ([P], SZ),
+        "pivot_paged_attention": ([P, P, P, SZ, P], I32),
+        "pivot_paged_attention_workspace_size": ([P, P], SZ),
+        "pivot_selected_attention": ([P, P, P, SZ, P], I32),
+        "pivot_selected_attention_workspace_size": ([P, P], SZ),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -463,6 +496,260 @@ def decode(batch: PivotDecode, mode, C, topk, want_cand=False, ws=None, stream=N
 
 def device_error(stream=None) -> int:
     return pivot_get_device_error(_stream(stream))
+
+
+# ---------------------------------------------------------------------------
+# paged key/value cache: append, pages, attention
+# ---------------------------------------------------------------------------
+
+def pivot_cache_append(cache, k_new, v_new, cu_new, total, max_new, lack, ws, ws_bytes, stream):
+    return load().pivot_cache_append(ctypes.byref(cache), k_new, v_new, cu_new, total, max_new,
+                                     lack, ws, ws_bytes, stream)
+
+
+def pivot_cache_append_workspace_size(cache, total):
+    return load().pivot_cache_append_workspace_size(ctypes.byref(cache), total)
+
+
+def pivot_pages_fork(cache, src, dst, n, ws, ws_bytes, stream):
+    return load().pivot_pages_fork(ctypes.byref(cache), src, dst, n, ws, ws_bytes, stream)
+
+
+def pivot_pages_fork_workspace_size(cache, n):
+    return load().pivot_pages_fork_workspace_size(ctypes.byref(cache), n)
+
+
+def pivot_pages_free(cache, seqs, keep, n, stream):
+    return load().pivot_pages_free(ctypes.byref(cache), seqs, keep, n, stream)
+
+
+def pivot_pages_copy(src, src_pages, dst, dst_pages, page_bytes, src_ids, dst_ids, n, stream):
+    return load().pivot_pages_copy(src, src_pages, dst, dst_pages, page_bytes, src_ids, dst_ids, n,
+                                   stream)
+
+
+def pivot_pages_compact(cache, remap, used, ws, ws_bytes, stream):
+    return load().pivot_pages_compact(ctypes.byref(cache), remap, used, ws, ws_bytes, stream)
+
+
+def pivot_pages_compact_workspace_size(cache):
+    return load().pivot_pages_compact_workspace_size(ctypes.byref(cache))
+
+
+def pivot_paged_attention(cache, call, ws, ws_bytes, stream):
+    return load().pivot_paged_attention(ctypes.byref(cache), ctypes.byref(call), ws, ws_bytes,
+                                        stream)
+
+
+def pivot_paged_attention_workspace_size(cache, call):
+    return load().pivot_paged_attention_workspace_size(ctypes.byref(cache), ctypes.byref(call))
+
+
+def pivot_selected_attention(cache, call, ws, ws_bytes, stream):
+    return load().pivot_selected_attention(ctypes.byref(cache), ctypes.byref(call), ws, ws_bytes,
+                                           stream)
+
+
+def pivot_selected_attention_workspace_size(cache, call):
+    return load().pivot_selected_attention_workspace_size(ctypes.byref(cache), ctypes.byref(call))
+
+
+class _On:
+    """The device of tensor `t` made current, and `stream` (None: that
+    device's current stream), for the length of a call: what the helpers
+    below allocate belongs to the stream that uses it."""
+
+    def __init__(self, t, stream):
+        self.ctx = []
+        if t.device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(t.device))
+        if stream is not None:
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _arg(t, name, dtype, shape, device):
+    """`t` if it is a contiguous tensor of that type, shape (None: any) and device; raises if not."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name}: a {dtype} tensor is wanted")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: wanted contiguous, on {device}")
+    return t
+
+
+def make_cache(k, v, table, length, refs, k_scale=None, v_scale=None) -> PivotCache:
+    """Describe a paged cache: k, v [num_pages, page_size, Hkv, D] bf16, or
+    e4m3 with k_scale, v_scale [num_pages, page_size]; table [B, max_pages],
+    length [B] and refs [num_pages] int32.  An empty cache has table -1,
+    length 0 and refs 0.  The struct keeps the tensors alive."""
+    if not k.is_cuda or k.dim() != 4 or table.dim() != 2:
+        raise ValueError("k: [num_pages, page_size, Hkv, D] on a CUDA device; table: [B, max_pages]")
+    n, page, Hkv, D = k.shape
+    B, columns = table.shape
+    dev, i32 = k.device, torch.int32
+    code = _dtype_code(k)
+    _arg(k, "k", k.dtype, k.shape, dev)
+    _arg(v, "v", k.dtype, k.shape, dev)
+    _arg(table, "table", i32, (B, columns), dev)
+    _arg(length, "length", i32, (B,), dev)
+    _arg(refs, "refs", i32, (n,), dev)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None:
+            _arg(t, name, torch.float32, (n, page), dev)
+    c = PivotCache(code, B, Hkv, D, page, n, columns, _p(k), _p(v), _p(k_scale), _p(v_scale),
+                   _p(table), _p(length), _p(refs))
+    c._keep = (k, v, k_scale, v_scale, table, length, refs)
+    return c
+
+
+def cache_append(cache: PivotCache, k_new, v_new, cu_new, max_new, ws=None, stream=None):
+    """Append rows cu_new[b] .. cu_new[b + 1] of k_new, v_new (bf16
+    [total, Hkv, D]) to sequence b; returns lack [1] int32 on the device: 0,
+    or the free pages missing (then nothing was appended)."""
+    dev = cache._keep[0].device
+    total = k_new.shape[0]
+    _arg(k_new, "k_new", torch.bfloat16, (total, cache.Hkv, cache.D), dev)
+    _arg(v_new, "v_new", torch.bfloat16, k_new.shape, dev)
+    _arg(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
+    with _On(k_new, stream) as st:
+        lack = torch.empty(1, dtype=torch.int32, device=dev)
+        if ws is None:
+            ws = _workspace(pivot_cache_append_workspace_size(cache, total), dev)
+        _check(pivot_cache_append(cache, _p(k_new), _p(v_new), _p(cu_new), total, max_new, _p(lack),
+                                  _p(ws), ws.numel(), st), "pivot_cache_append")
+    return lack
+
+
+def pages_fork(cache: PivotCache, src, dst, ws=None, stream=None):
+    """Make sequence dst[i] a copy of sequence src[i] as it stood before the
+    call, its pages shared; src, dst [n] int32, dst distinct."""
+    dev, n = cache._keep[0].device, src.shape[0]
+    _arg(src, "src", torch.int32, (n,), dev)
+    _arg(dst, "dst", torch.int32, (n,), dev)
+    with _On(src, stream) as st:
+        if ws is None:
+            ws = _workspace(pivot_pages_fork_workspace_size(cache, n), dev)
+        _check(pivot_pages_fork(cache, _p(src), _p(dst), n, _p(ws), ws.numel(), st),
+               "pivot_pages_fork")
+
+
+def pages_free(cache: PivotCache, seqs, keep, stream=None):
+    """Cut sequence seqs[i] to its first keep[i] tokens (0: free it); seqs
+    distinct."""
+    dev, n = cache._keep[0].device, seqs.shape[0]
+    _arg(seqs, "seqs", torch.int32, (n,), dev)
+    _arg(keep, "keep", torch.int32, (n,), dev)
+    with _On(seqs, stream) as st:
+        _check(pivot_pages_free(cache, _p(seqs), _p(keep), n, st), "pivot_pages_free")
+
+
+def pages_copy(src, dst, src_ids, dst_ids, stream=None):
+    """dst[dst_ids[i]] = src[src_ids[i]] for planes whose first axis counts
+    pages; ids [n] int32, no destination named twice or read in the same call."""
+    dev, n = src.device, src_ids.shape[0]
+    if src.dtype != dst.dtype or src.shape[1:] != dst.shape[1:]:
+        raise ValueError("src and dst: pages of one type and shape")
+    _arg(src, "src", src.dtype, src.shape, dev)
+    _arg(dst, "dst", src.dtype, dst.shape, dev)
+    _arg(src_ids, "src_ids", torch.int32, (n,), dev)
+    _arg(dst_ids, "dst_ids", torch.int32, (n,), dev)
+    with _On(src, stream) as st:
+        page = src[0].numel() * src.element_size()
+        _check(pivot_pages_copy(_p(src), src.shape[0], _p(dst), dst.shape[0], page, _p(src_ids),
+                                _p(dst_ids), n, st), "pivot_pages_copy")
+
+
+def pages_compact(cache: PivotCache, ws=None, stream=None):
+    """Move the pages in use to the lowest ids; returns (remap [num_pages]:
+    each used page's new id, -1 for free ones; used [1])."""
+    dev = cache._keep[0].device
+    with _On(cache._keep[0], stream) as st:
+        remap = torch.empty(cache.num_pages, dtype=torch.int32, device=dev)
+        used = torch.empty(1, dtype=torch.int32, device=dev)
+        if ws is None:
+            ws = _workspace(pivot_pages_compact_workspace_size(cache), dev)
+        _check(pivot_pages_compact(cache, _p(remap), _p(used), _p(ws), ws.numel(), st),
+               "pivot_pages_compact")
+    return remap, used
+
+
+def _attention(cache, q, cu_new, max_new, idx, scale, window, with_lse, o, ws, stream):
+    dev = cache._keep[0].device
+    total, Hq = q.shape[0], q.shape[1]
+    _arg(q, "q", torch.bfloat16, (total, Hq, cache.D), dev)
+    _arg(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
+    topk = 0
+    if idx is not None:
+        topk = idx.shape[-1]
+        _arg(idx, "idx", torch.int32, (total, topk), dev)
+    if o is not None:
+        _arg(o, "o", torch.bfloat16, q.shape, dev)
+    name = "pivot_paged_attention" if idx is None else "pivot_selected_attention"
+    lib = load()
+    with _On(q, stream) as st:
+        if o is None:
+            o = torch.empty_like(q)
+        lse = torch.empty(total, Hq, dtype=torch.float32, device=dev) if with_lse else None
+        call = PivotAttend(Hq, total, max_new, _p(q), _p(cu_new),
+                           cache.D ** -0.5 if scale is None else scale, window, _p(idx), topk,
+                           _p(o), _p(lse))
+        if ws is None:
+            ws = _workspace(getattr(lib, name + "_workspace_size")(ctypes.byref(cache),
+                                                                   ctypes.byref(call)), dev)
+        _check(getattr(lib, name)(ctypes.byref(cache), ctypes.byref(call), _p(ws), ws.numel(), st),
+               name)
+    return o, lse
+
+
+def paged_attention(cache: PivotCache, q, cu_new, max_new, scale=None, window=0, with_lse=False,
+                    o=None, ws=None, stream=None):
+    """Causal attention of the batch's new tokens (q bf16 [total, Hq, D], rows
+    cu_new[b] .. cu_new[b + 1] the last tokens of sequence b, already
+    appended) over the cache; window > 0 keeps that many positions up to the
+    token's own.  scale: 1 / sqrt(D) by default.  Returns (o, lse or None);
+    rows behind cu_new[B] are left as they were."""
+    return _attention(cache, q, cu_new, max_new, None, scale, window, with_lse, o, ws, stream)
+
+
+def selected_attention(cache: PivotCache, q, cu_new, max_new, idx, scale=None, with_lse=False,
+                       o=None, ws=None, stream=None):
+    """paged_attention over the positions of idx [total, topk] (-1 padded), as
+    dense_index, reuse, refine, decode ... return them."""
+    return _attention(cache, q, cu_new, max_new, idx, scale, 0, with_lse, o, ws, stream)
+
+
+def decode_attention(batch: PivotDecode, cache: PivotCache, q, k_new, v_new, mode, C, topk,
+                     scale=None, with_lse=False, stream=None):
+    """One sparse decode step of a model's layer: the Gm new tokens of every
+    sequence are appended to the cache (k_new, v_new bf16
+    [B, Gm, Hkv, D]), the indexer (`decode`, mode DENSE, REUSE or REFINE)
+    names each token's positions, and attention (q bf16 [B, Gm, Hq, D])
+    reads them.  batch.cache_len counts the new tokens: the lengths that the
+    append leaves (it may be the cache's own length tensor).  Returns
+    (o [B, Gm, Hq, D], lse or None, idx, lack); a lack above 0 (on the
+    device) says that the pages ran out and o is not to be used."""
+    B, Gm = batch.B, batch.Gm
+    dev = cache._keep[0].device
+    if cache.B != B or tuple(q.shape[:2]) != (B, Gm):
+        raise ValueError("batch, cache and q: one number of sequences and of new tokens")
+    with _On(q, stream):
+        cu = torch.arange(0, (B + 1) * Gm, Gm, dtype=torch.int32, device=dev)
+        lack = cache_append(cache, k_new.reshape(B * Gm, cache.Hkv, cache.D),
+                            v_new.reshape(B * Gm, cache.Hkv, cache.D), cu, Gm)
+        idx, _ = decode(batch, mode, C, topk, device=dev)
+        o, lse = selected_attention(cache, q.reshape(B * Gm, q.shape[2], cache.D), cu, Gm,
+                                    idx.view(B * Gm, topk), scale=scale, with_lse=with_lse)
+    return o.view(q.shape), None if lse is None else lse.view(B, Gm, -1), idx, lack
 
 
 # ---------------------------------------------------------------------------
