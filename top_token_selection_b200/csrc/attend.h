@@ -144,6 +144,7 @@ size_t attend_part_bytes(int ncta, int R, int D);
 
 cudaError_t launch_attend_plan(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_rows(const AttendParams& p, cudaStream_t st);
+cudaError_t launch_attend_umma(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t st);
 
 // CTAs and tile of the rows kernel.

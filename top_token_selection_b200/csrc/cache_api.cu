@@ -88,12 +88,19 @@ pivot_status_t check_attend(const pivot_cache_t* cache, const pivot_attend_t* a,
     p->window = a->window;
     p->topk = a->topk;
     p->scale_log2 = a->scale * 1.4426950408889634f;
-    // rows a sequence has for one key/value head: 16 at a time, or 32, so
-    // that a key is read once for up to 32 of them
+    // Rows a sequence has for one key/value head: up to 32 on the warp-level
+    // kernel (16 or 32 of them share each key read), more on the tensor-memory
+    // kernel in blocks of 128 or 256.
     const long long rows = selected ? p->G : (long long)p->max_new * p->G;
-    p->R = rows <= 16 ? 16 : 32;
-    p->TK = rows_tile(cache->dtype);
-    p->ncta = sm_count() * ROWS_CTAS_PER_SM;
+    if (rows > 32) {
+        p->R = selected || rows <= 128 ? 128 : 256;
+        p->TK = 128;
+        p->ncta = sm_count();
+    } else {
+        p->R = rows <= 16 ? 16 : 32;
+        p->TK = rows_tile(cache->dtype);
+        p->ncta = sm_count() * ROWS_CTAS_PER_SM;
+    }
     return PIVOT_OK;
 }
 
@@ -132,7 +139,7 @@ pivot_status_t attend(const pivot_cache_t* cache, const pivot_attend_t* a, bool 
         if (e != cudaSuccess) return status_of(e);
     }
     count_launch();
-    e = launch_attend_rows(p, st);
+    e = p.R > 32 ? launch_attend_umma(p, st) : launch_attend_rows(p, st);
     if (e != cudaSuccess) return status_of(e);
     count_launch();
     return status_of(launch_attend_join(p, st));
