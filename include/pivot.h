@@ -441,9 +441,12 @@ size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
  * are what the indexer's calls write, in either order.
  * Slots past a sequence's tokens may hold anything; the tokens' own stored
  * keys and values are finite.  Rows of o and lse from cu_new[B] on stay as
- * they were.  Products of bf16 keys and values run on the tensor cores with
- * fp32 sums; softmax statistics and sums are fp32; weights are rounded to
- * bf16 for the product with V.  scale: any positive finite value. */
+ * they were.  Products run on the tensor cores with fp32
+ * sums, and the softmax in fp32.  Rounded are the weights of the product with
+ * V: to bf16 beside bf16 values; to f16 beside e4m3 codes, which go into the
+ * products exactly, as f16, with their scales in fp32 (a value whose scale
+ * is below 2^-14 of the largest of its tile of 32 to 128 tokens loses bits).
+ * scale: any positive finite value. */
 typedef struct {
     int32_t Hq;                  /* query heads, a multiple of Hkv               */
     int32_t total;               /* rows of q                                    */

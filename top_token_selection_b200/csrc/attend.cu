@@ -95,13 +95,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
     return r;
 }
-__device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t h) {
-    float lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-    return bf16x2(lo, hi);
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -476,11 +469,14 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                         s[mt][n][e] = x;
                     }
 
-            // ---- running maximum; the sums move only when it grew
+            // ---- running maximum (e4m3: of weight times value scale, see
+            // log2_above); the sums move only when it grew
+            float lv = 0.0f;
+            if constexpr (FP8) lv = log2_above(sc[KW + lane]);
             uint32_t pf[MT][NT / 2][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                float mx[2] = {m[mt][0], m[mt][1]};
+                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     mx[0] = fmaxf(mx[0], fmaxf(s[mt][n][0], s[mt][n][1]));
@@ -490,6 +486,8 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                 for (int e = 0; e < 2; ++e) {
                     mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
                     mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                    if constexpr (FP8) mx[e] += lv;
+                    mx[e] = fmaxf(mx[e], m[mt][e]);
                 }
                 if (__any_sync(0xffffffffu, mx[0] != m[mt][0] || mx[1] != m[mt][1])) {
 #pragma unroll
@@ -512,8 +510,9 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                     float e2 = ex2(s[mt][n][2] - z1), e3 = ex2(s[mt][n][3] - z1);
                     // the sum takes the weights as they are (the log-sum-exp
                     // is wanted in fp32); for the product they keep the 8 bits
-                    // of the bf16 values they meet: an error of at most 2^-8
-                    // of each weight, independent from key to key
+                    // of the bf16 values they meet (an error of at most 2^-8
+                    // of each weight, independent from key to key), or the 11
+                    // of f16 beside e4m3 values, which f16 holds exactly
                     l[mt][0] += e0 + e1;
                     l[mt][1] += e2 + e3;
                     if constexpr (FP8) {
@@ -521,7 +520,8 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                         const float2 v = *reinterpret_cast<const float2*>(sc + KW + n * 8 + c4 * 2);
                         e0 *= v.x; e1 *= v.y; e2 *= v.x; e3 *= v.y;
                     }
-                    const uint32_t lo = bf16x2(e0, e1), hi = bf16x2(e2, e3);
+                    const uint32_t lo = FP8 ? f16x2(e0, e1) : bf16x2(e0, e1);
+                    const uint32_t hi = FP8 ? f16x2(e2, e3) : bf16x2(e2, e3);
                     pf[mt][n >> 1][(n & 1) * 2] = lo;
                     pf[mt][n >> 1][(n & 1) * 2 + 1] = hi;
                 }
@@ -539,15 +539,15 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t w = __byte_perm(r[i], 0, 0x3120);
-                        even[i] = f16x2_bf16x2(e4m3x2_f16x2((uint16_t)(w & 0xFFFFu)));
-                        odd[i] = f16x2_bf16x2(e4m3x2_f16x2((uint16_t)(w >> 16)));
+                        even[i] = e4m3x2_f16x2((uint16_t)(w & 0xFFFFu));
+                        odd[i] = e4m3x2_f16x2((uint16_t)(w >> 16));
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        mma_bf16(acc[mt][2 * ch], pf[mt][0], even[0], even[1]);
-                        mma_bf16(acc[mt][2 * ch], pf[mt][1], even[2], even[3]);
-                        mma_bf16(acc[mt][2 * ch + 1], pf[mt][0], odd[0], odd[1]);
-                        mma_bf16(acc[mt][2 * ch + 1], pf[mt][1], odd[2], odd[3]);
+                        mma_f16(acc[mt][2 * ch], pf[mt][0], even[0], even[1]);
+                        mma_f16(acc[mt][2 * ch], pf[mt][1], even[2], even[3]);
+                        mma_f16(acc[mt][2 * ch + 1], pf[mt][0], odd[0], odd[1]);
+                        mma_f16(acc[mt][2 * ch + 1], pf[mt][1], odd[2], odd[3]);
                     }
                 }
             } else {

@@ -136,6 +136,18 @@ __device__ __forceinline__ Item find_item(const AttendParams& p, long long u) {
     return it;
 }
 
+// For the value scales of a warp's 32 keys: the log2 of the power of two at
+// or above their largest size, within [-100, 100] (0 if all are 0).  The
+// reference point of an e4m3 softmax is raised by it, so that weight times
+// scale is at most 1 (f16 keeps 11 bits of it down to 2^-14 and an absolute
+// 2^-25 below), and l and o stay in the same units.
+__device__ __forceinline__ float log2_above(float scale) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(scale)));
+    if (top == 0) return 0.0f;
+    const int e = (int)((top + 0x007FFFFFu) >> 23) - 127;
+    return (float)(e < -100 ? -100 : e > 100 ? 100 : e);
+}
+
 __device__ __forceinline__ size_t slot_words(int R, int D) { return (size_t)R * (D + 2); }
 
 // Bytes of the plan and of the partial sums.

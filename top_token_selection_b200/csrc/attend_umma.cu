@@ -5,8 +5,9 @@
 // S = Q K^T and O += P V by tcgen05.mma with the accumulators in TMEM:
 // 128 query rows on the M axis (the 128 TMEM lanes), so one thread owns one
 // row's softmax and no shuffle is needed; 128 keys a tile.  P goes back to
-// TMEM as bf16, over the S it came from, and is the A operand of the second
-// product.  Two such tiles are in flight and take turns: while one's softmax
+// TMEM in 16 bits, over the S it came from, and is the A operand of the second
+// product (bf16 beside bf16 values; e4m3 codes are converted to f16, which
+// holds them exactly, and P is f16 then).  Two such tiles are in flight and take turns: while one's softmax
 // runs, the tensor cores work on the other.  They are
 //  * the two halves of a block of 256 rows, which share every key tile; or
 //  * (SPLIT) the even and odd key tiles of one block of up to 128 rows, each
@@ -47,13 +48,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
     return r;
-}
-__device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t h) {
-    float lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-    return bf16x2(lo, hi);
 }
 __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool live) {
     const int n = live ? 16 : 0;
@@ -108,7 +102,7 @@ struct UmmaShape {
     // has a ring slot, which is after its readers are done: 2 MS > STAGES.
     static constexpr int MS = 8;
     static_assert(2 * MS > STAGES, "meta slots outlive the ring");
-    static constexpr int META = MS * (16 + (FP8 ? TKEYS * 8 : 0));
+    static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 8 : 0));
     static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + META + 512;
 };
 
@@ -125,7 +119,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
     uint8_t* sC = sT + STAGES * S::TILE;                  // e4m3 codes on their way
     uint8_t* sM = sC + S::STAGING;
     uint32_t* m_ok = reinterpret_cast<uint32_t*>(sM);     // [MS][4]
-    float* m_ks = reinterpret_cast<float*>(sM + MS * 16); // [MS][128]
+    float* m_lv = reinterpret_cast<float*>(sM + MS * 16); // [MS][4] see log2_above
+    float* m_ks = m_lv + MS * 4;                          // [MS][128]
     float* m_vs = m_ks + MS * TKEYS;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sM + S::META);
     uint64_t* full = bars;                                // [STAGES] tile there
@@ -138,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
     uint64_t* drain = qfull + 1;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -212,17 +207,24 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                 page_a[g] = page_of(pos_a[g]);
                 pos_b[g] = position(x + 3, g);
             }
-            // token row of key g * 32 + lane of tile x; then x + 3's is under way
-            auto resolve = [&](int x, int g) -> int {
-                int row = -1;
-                if (page_a[g] != -2) {
-                    row = p.c.row_of(page_a[g], pos_a[g]);
-                    if (row < 0) raise_error(ERRBIT_DATA);
+            // Token rows of this lane's keys of tile x; the next own tile's
+            // pages and the positions after it are then under way.  All waits
+            // come before all loads: a load waited for beside younger ones
+            // costs their latency too.
+            auto resolve = [&](int x, int (&row)[4]) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    row[g] = -1;
+                    if (page_a[g] != -2) {
+                        row[g] = p.c.row_of(page_a[g], pos_a[g]);
+                        if (row[g] < 0) raise_error(ERRBIT_DATA);
+                    }
+                    pos_a[g] = pos_b[g];
                 }
-                pos_a[g] = pos_b[g];
-                page_a[g] = page_of(pos_a[g]);
-                pos_b[g] = position(x + 6, g);
-                return row;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) page_a[g] = page_of(pos_a[g]);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) pos_b[g] = position(x + 6, g);
             };
             auto wait_slot = [&](long long e) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait(&empty[e % STAGES], (uint32_t)((e / STAGES) & 1) ^ 1));
@@ -237,11 +239,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                     const long long e = entry0 + x;
                     int row[4];
                     uint32_t ok[4];
+                    resolve(x, row);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        row[g] = resolve(x, g);
-                        ok[g] = __ballot_sync(0xffffffffu, row[g] >= 0);
-                    }
+                    for (int g = 0; g < 4; ++g) ok[g] = __ballot_sync(0xffffffffu, row[g] >= 0);
                     if (!wait_slot(e)) { aborted = true; break; }
                     if ((x & 1) == 0 && lane < 4)
                         m_ok[((tile_no + (x >> 1)) % MS) * 4 + lane] =
@@ -267,26 +267,35 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                 // keys takes the same keys of the warp's next tile at once.  A
                 // lane converts the chunks that it copied itself.
                 const uint32_t mine = smem_u32(sC) + lw * (TKEYS * D) + lane * 16;
-                float ks[4], vs[4];                        // of the tile in staging
-                uint32_t ok[4];
+                int row[4];                                // of the tile being copied
+                float ks[4], vs[4], ks_n[4], vs_n[4];      // of the tile in staging, and of the next
+                uint32_t ok[4], ok_n[4];
+                auto look_up = [&](int x) {
+                    if (x >= total) return;
+                    resolve(x, row);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        ok_n[g] = __ballot_sync(0xffffffffu, row[g] >= 0);
+                        ks_n[g] = vs_n[g] = 0.0f;
+                        if ((x & 1) == 0 && row[g] >= 0) {
+                            ks_n[g] = ld_nc_early(p.c.ks + row[g]);
+                            vs_n[g] = ld_nc_early(p.c.vs + row[g]);
+                        }
+                    }
+                };
                 auto load = [&](int x, int g) {
                     if (x < total) {
-                        const int row = resolve(x, g);
-                        if ((x & 1) == 0) {
-                            ok[g] = __ballot_sync(0xffffffffu, row >= 0);
-                            ks[g] = row >= 0 ? ld_nc_early(p.c.ks + row) : 0.0f;
-                            vs[g] = row >= 0 ? ld_nc_early(p.c.vs + row) : 0.0f;
-                        }
                         const uint8_t* plane = ((x & 1) ? p.c.v : p.c.k) + head_off;
 #pragma unroll
                         for (int i = 0; i < 32 / KPI; ++i) {
-                            const int r = __shfl_sync(0xffffffffu, row, i * KPI + sub);
+                            const int r = __shfl_sync(0xffffffffu, row[g], i * KPI + sub);
                             cp16_or_zero(mine + g * (32 * D) + i * 512,
                                          plane + (size_t)(r < 0 ? 0 : r) * p.c.rowb, r >= 0);
                         }
                     }
                     cp_async_commit();
                 };
+                look_up(x);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) load(x, g);
                 for (; x < total; x += 3) {
@@ -295,28 +304,37 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                     const int ms = (tile_no + (x >> 1)) % MS;
                     const uint32_t dst = smem_u32(sT + (e % STAGES) * S::TILE) + (ch >> 2) * (TKEYS * 128);
 #pragma unroll
+                    for (int g = 0; g < 4; ++g) { ks[g] = ks_n[g]; vs[g] = vs_n[g]; ok[g] = ok_n[g]; }
+                    look_up(x + 3);
+#pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         cp_async_wait<3>();
                         if ((x & 1) == 0) {
-                            if (lane == 0) m_ok[ms * 4 + g] = ok[g];
+                            const float lv = log2_above(vs[g]);
+                            if (lane == 0) {
+                                m_ok[ms * 4 + g] = ok[g];
+                                m_lv[ms * 4 + g] = lv;
+                            }
                             m_ks[ms * TKEYS + g * 32 + lane] = ks[g];
                             m_vs[ms * TKEYS + g * 32 + lane] = vs[g];
                         }
+                        // all of the group's reads come first: stores between
+                        // them would hold each up behind the last one's chain
+                        uint4 w[32 / KPI];
 #pragma unroll
-                        for (int i = 0; i < 32 / KPI; ++i) {
-                            uint32_t w[4], y[8];
+                        for (int i = 0; i < 32 / KPI; ++i)
                             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
                                          : "r"(mine + g * (32 * D) + i * 512)
                                          : "memory");
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                y[2 * k] = e4m3x2_f16x2((uint16_t)(w[k] & 0xFFFFu));
-                                y[2 * k + 1] = e4m3x2_f16x2((uint16_t)(w[k] >> 16));
-                            }
-                            if (x & 1) {
+                        for (int i = 0; i < 32 / KPI; ++i) {
+                            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                            uint32_t y[8];
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) y[k] = f16x2_bf16x2(y[k]);
+                            for (int k = 0; k < 4; ++k) {
+                                y[2 * k] = e4m3x2_f16x2((uint16_t)(v[k] & 0xFFFFu));
+                                y[2 * k + 1] = e4m3x2_f16x2((uint16_t)(v[k] >> 16));
                             }
                             const int r = g * 32 + i * KPI + sub, c0 = 2 * (ch & 3);
                             // the upper 64 values' lanes write their second half
@@ -338,73 +356,87 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
         }
         cp_async_wait<0>();
     } else if (warp == MMA_WARP) {
-        if (lane == 0) {
-            // --------------------------------------------------------- MMA
-            const uint32_t id_s = make_idesc(FP8 ? 0u : 1u, 128, TKEYS);       // Q K^T: f16 / bf16
-            const uint32_t id_o = make_idesc(1u, 128, D) | (1u << 16);         // P V: bf16, V's N contiguous
-            const uint32_t q0 = smem_u32(sQ), t0 = smem_u32(sT);
-            long long entry = 0;
-            long long tile_no = 0;
-            uint32_t steps[2] = {0, 0};      // P handed over so far, per tile
-            uint32_t items = 0;
-            bool aborted = false;
-            for (long long u = u_begin; u < u_end && !aborted;) {
-                const Item it = find_item<SELECTED>(p, u);
-                const int ta = it.tile0 + (int)(u - it.unit0);
-                const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
-                u = it.unit0 + (tz - it.tile0);
-                if (!it.ok) continue;
-                const int n = tz - ta, H = SPLIT ? n : 2 * n;
-                if (!mbar_wait(qfull, items & 1)) break;
-                ++items;
-                tc_fence_after();
-                auto wait_tile = [&](long long e) -> bool {
-                    const bool r = mbar_wait(&full[e % STAGES], (uint32_t)((e / STAGES) & 1));
-                    tc_fence_after();
-                    return r;
-                };
-                auto do_s = [&](int h) -> bool {
-                    const int t = h & 1, j = SPLIT ? h : h >> 1;
-                    const long long e = entry + 2 * j;
-                    if (SPLIT || t == 0) {
-                        if (!wait_tile(e)) return false;
-                        mbar_arrive(&mfull[(tile_no + j) % MS]);
-                    }
-                    const uint32_t a = q0 + (SPLIT ? 0 : t * S::TILE);
-                    const uint32_t b = t0 + (uint32_t)(e % STAGES) * S::TILE;
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * (TKEYS * 128) + (ks & 3) * 32;
-                        umma_ss<KIND_F16>(tmem + t * 128, smem_desc_k_sw128(a + off),
-                                          smem_desc_k_sw128(b + off), id_s, ks > 0);
-                    }
-                    umma_commit(&sfull[t]);
-                    if (SPLIT || t == 1) umma_commit(&empty[e % STAGES]);
-                    return true;
-                };
-                aborted = !do_s(0) || (H > 1 && !do_s(1));
-                for (int h = 0; h < H && !aborted; ++h) {
-                    const int t = h & 1, j = SPLIT ? h : h >> 1;
-                    const long long e = entry + 2 * j + 1;
-                    if (!mbar_wait(&pfull[t], steps[t] & 1)) { aborted = true; break; }
-                    ++steps[t];
-                    if ((SPLIT || t == 0) && !wait_tile(e)) { aborted = true; break; }
-                    tc_fence_after();
-                    const uint32_t b = t0 + (uint32_t)(e % STAGES) * S::TILE;
-#pragma unroll
-                    for (int ks = 0; ks < TKEYS / 16; ++ks)
-                        umma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8,
-                                smem_desc_mn_sw128(b + ks * 2048), id_o, h > 1 || ks > 0);
-                    if (SPLIT || t == 1) umma_commit(&empty[e % STAGES]);
-                    if (h + 2 >= H) umma_commit(&ofull[t]);
-                    else if (!do_s(h + 2)) aborted = true;
-                }
-                entry += 2 * n;
-                tile_no += n;
+        // ------------------------------------------------------------- MMA
+        // The whole warp walks the steps and one lane issues: descriptors
+        // then stay in uniform registers.  (Issued from inside a one-lane
+        // branch an MMA took about 140 cycles to issue, twice its own time.)
+        const bool leader = elect_one();
+        const uint32_t id_s = make_idesc(FP8 ? 0u : 1u, 128, TKEYS);            // Q K^T
+        const uint32_t id_o = make_idesc(FP8 ? 0u : 1u, 128, D) | (1u << 16);   // P V: V's N contiguous
+        const uint64_t dq = smem_desc_k_sw128(smem_u32(sQ));
+        const uint64_t dk = smem_desc_k_sw128(smem_u32(sT)), dv = smem_desc_mn_sw128(smem_u32(sT));
+        constexpr uint32_t TILE16 = S::TILE >> 4;      // descriptor addresses count 16 bytes
+        // ring positions of the next K and V tiles, and their phases
+        uint32_t ks = 0, kph = 0, vs = 1, vph = 0, ms = 0;
+        auto next = [](uint32_t& slot, uint32_t& ph) {
+            slot += 2;
+            if (slot >= STAGES) {
+                slot -= STAGES;
+                ph ^= 1;
             }
+        };
+        uint32_t pph[2] = {0, 0};        // phase of the next P, per tile
+        uint32_t qph = 0;
+        bool aborted = false;
+        // S of tile t from the K tile at hand; `last`: no other product needs it
+        auto do_s = [&](int t) -> bool {
+            if (SPLIT || t == 0) {
+                if (!mbar_wait(&full[ks], kph)) return false;
+                tc_fence_after();
+                if (leader) mbar_arrive(&mfull[ms]);
+                ms = (ms + 1) % MS;
+            }
+            if (leader) {
+                const uint64_t a = dq + (SPLIT ? 0 : t * TILE16), b = dk + ks * TILE16;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t off = ((i >> 2) * (TKEYS * 128) + (i & 3) * 32) >> 4;
+                    umma_ss<KIND_F16>(tmem + t * 128, a + off, b + off, id_s, i > 0);
+                }
+                umma_commit(&sfull[t]);
+                if (SPLIT || t == 1) umma_commit(&empty[ks]);
+            }
+            __syncwarp();
+            if (SPLIT || t == 1) next(ks, kph);
+            return true;
+        };
+        for (long long u = u_begin; u < u_end && !aborted;) {
+            const Item it = find_item<SELECTED>(p, u);
+            const int ta = it.tile0 + (int)(u - it.unit0);
+            const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
+            u = it.unit0 + (tz - it.tile0);
+            if (!it.ok) continue;
+            const int n = __shfl_sync(0xffffffffu, tz - ta, 0), H = SPLIT ? n : 2 * n;
+            if (!mbar_wait(qfull, qph)) break;
+            qph ^= 1;
+            tc_fence_after();
+            aborted = !do_s(0) || (H > 1 && !do_s(1));
+            auto step = [&](int h, int t) -> bool {
+                if (!mbar_wait(&pfull[t], pph[t])) return false;
+                pph[t] ^= 1;
+                if ((SPLIT || t == 0) && !mbar_wait(&full[vs], vph)) return false;
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t b = dv + vs * TILE16;
+#pragma unroll
+                    for (int i = 0; i < TKEYS / 16; ++i)
+                        umma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, b + i * (2048 >> 4), id_o,
+                                i > 0 ? 1u : (uint32_t)(h > 1));
+                    if (SPLIT || t == 1) umma_commit(&empty[vs]);
+                    if (h + 2 >= H) umma_commit(&ofull[t]);
+                }
+                __syncwarp();
+                if (SPLIT || t == 1) next(vs, vph);
+                return h + 2 >= H || do_s(t);
+            };
+            for (int h = 0; h < H && !aborted; h += 2)
+                aborted = !step(h, 0) || (h + 1 < H && !step(h + 1, 1));
+        }
+        if (leader) {
             umma_commit(drain);
             mbar_wait(drain, 0);
         }
+        __syncwarp();
     } else {
         // --------------------------------------------------------- softmax
         const int t = warp >> 2;
@@ -535,10 +567,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                     mx[2] = fmaxf(mx[2], s[k + 2]);
                     mx[3] = fmaxf(mx[3], s[k + 3]);
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                if constexpr (FP8) {
+                    const float4 lv = *reinterpret_cast<const float4*>(m_lv + ms * 4);
+                    top += fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
+                }
                 // The reference point m may lag behind the maximum by up to
                 // 8: weights then reach 2^8, which costs no precision, and
-                // the sums in TMEM seldom have to be multiplied.
+                // the sums in TMEM seldom have to be multiplied.  For e4m3
+                // it stands over the weights times the values' scales, so
+                // that their product fits f16 whatever the scales; the sums
+                // of both are in its units, which cancel in o.
                 float f = 1.0f;
                 if (top > m + 8.0f) {
                     f = m == -INFINITY ? 0.0f : ex2(m - top);
@@ -586,8 +625,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                             const float4 v = vs[(i * 32 + k) / 4];
                             e[0] *= v.x; e[1] *= v.y; e[2] *= v.z; e[3] *= v.w;
                         }
-                        pk[k / 2] = bf16x2(e[0], e[1]);
-                        pk[k / 2 + 1] = bf16x2(e[2], e[3]);
+                        pk[k / 2] = FP8 ? f16x2(e[0], e[1]) : bf16x2(e[0], e[1]);
+                        pk[k / 2 + 1] = FP8 ? f16x2(e[2], e[3]) : bf16x2(e[2], e[3]);
                     }
                     tmem_st16(tS + i * 16, pk);
                 }
