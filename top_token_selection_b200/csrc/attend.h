@@ -156,7 +156,11 @@ size_t attend_part_bytes(int ncta, int R, int D);
 
 cudaError_t launch_attend_plan(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_rows(const AttendParams& p, cudaStream_t st);
-cudaError_t launch_attend_umma(const AttendParams& p, cudaStream_t st);
+// tk, tv: the planes as token rows x Hkv D values, boxes of a page (at
+// most 128 tokens) and one head's codes or 64 bf16 values, 128-byte swizzle
+// for 128-byte rows
+cudaError_t launch_attend_umma(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p,
+                               cudaStream_t st);
 cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t st);
 
 // CTAs and tile of the rows kernel.

@@ -15,10 +15,14 @@
 //
 // TMEM (512 columns): S/P of tile 0, S/P of tile 1, O of tile 0, O of tile 1.
 //
-// Warps 0-3 and 4-7: softmax of tiles 0 and 1.  Warps 8-10: loads, every
-// third K or V tile each.  Warp 11: MMA issue.  Three warps on each of the
-// SM's four register files leave 168 registers a thread: the softmax holds
-// its row's 128 scores.
+// Paged keys come by TMA, a page a box.  Selected keys are copied row by row
+// with cp.async (tile::gather4 was measured: about 75 cycles for four 128-byte
+// rows, a quarter of what the products take).
+//
+// Warps 0-3 and 4-7: softmax of tiles 0 and 1.  Warp 8: rows and TMA loads.
+// Warps 9 and 10: copies of selected keys, e4m3 codes to halves.  Warp 11:
+// MMA issue.  Three warps on each of the SM's four register files leave 168
+// registers a thread: the softmax holds its row's 128 scores.
 #include "attend.h"
 
 namespace pivot {
@@ -49,13 +53,35 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
     return r;
 }
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool live) {
-    const int n = live ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ void sts16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 2^x of a number of at most 2^7 on the FMA pipe: x = n + f with n whole and
+// |f| <= 1/2 (the sum with 3 2^22 rounds to whole numbers), then a polynomial
+// of degree 4 for 2^f with value 1 at 0, fitted for the least relative error
+// (2.8e-6), and n added to the exponent.  Below -126 the result is 2^-126.
+__device__ __forceinline__ float exp2_poly(float x) {
+    x = fmaxf(x, -126.0f);
+    const float t = x + 12582912.0f;
+    const float f = x - (t - 12582912.0f);
+    float y = fmaf(f, 0.009582852944731712f, 0.055906426161527634f);
+    y = fmaf(y, f, 0.24024099111557007f);
+    y = fmaf(y, f, 0.6931241750717163f);
+    y = fmaf(y, f, 1.0f);
+    return __uint_as_float(__float_as_uint(y) + (__float_as_uint(t) << 23));
+}
+
 // 16 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -67,6 +93,61 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& a, uint32_t& b) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Weights 2^(c s + z) of 64 keys of a row: to TMEM in 16 bits (times the
+// values' scales for e4m3), and their sum.  The special-function unit gives
+// 16 exponentials a clock, which would take as long as the tile's products;
+// in a tile without masks POLY of every 16 are computed on the FMA pipe.
+constexpr int POLY = 4;
+template <bool FP8, bool PLAIN>
+__device__ __forceinline__ float weights(float* s, float c, float z, const float* vs, uint32_t to) {
+    const uint64_t c2 = pack2(c, c), z2 = pack2(z, z);
+    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            float* x = s + i * 32 + k;
+            float e[4];
+#pragma unroll
+            for (int y = 0; y < 4; y += 2) {
+                const uint64_t v = ffma2(pack2(x[y], x[y + 1]), c2, z2);
+                unpack2(v, e[y], e[y + 1]);
+                const bool poly = PLAIN && (k + y) % 16 < POLY;
+                e[y] = poly ? exp2_poly(e[y]) : ex2(e[y]);
+                e[y + 1] = poly ? exp2_poly(e[y + 1]) : ex2(e[y + 1]);
+                sum[y / 2] = add2(sum[y / 2], pack2(e[y], e[y + 1]));
+            }
+            if constexpr (FP8) {
+                const float4 v = *reinterpret_cast<const float4*>(vs + i * 32 + k);
+                e[0] *= v.x; e[1] *= v.y; e[2] *= v.z; e[3] *= v.w;
+            }
+            pk[k / 2] = FP8 ? f16x2(e[0], e[1]) : bf16x2(e[0], e[1]);
+            pk[k / 2 + 1] = FP8 ? f16x2(e[2], e[3]) : bf16x2(e[2], e[3]);
+        }
+        tmem_st16(to + i * 16, pk);
+    }
+    float a, b, d, e;
+    unpack2(sum[0], a, b);
+    unpack2(sum[1], d, e);
+    return (a + b) + (d + e);
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
@@ -90,64 +171,82 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
     return d;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool SELECTED, bool SPLIT>
 struct UmmaShape {
     static constexpr int TILE = TKEYS * D * 2;               // K or V tile, and 128 rows of Q
-    static constexpr int STAGES = FP8 ? 3 : (D == 128 ? 5 : 8);
-    // e4m3 codes wait in a staging tile of each load warp and are converted
-    // from there; bf16 goes into the tile directly
-    static constexpr int STAGING = FP8 ? 3 * TKEYS * D : 0;
-    // per tile what the softmax needs besides S: which keys count, and for
-    // e4m3 their scales.  A slot is written again once the K tile MS later
-    // has a ring slot, which is after its readers are done: 2 MS > STAGES.
+    static constexpr int QTILES = SPLIT ? 1 : 2;
+    // ring slots: as many as fit beside Q (and the staging tiles)
+    static constexpr int STAGES = D == 64 ? 8 : (FP8 ? 3 : 5) + (SPLIT && (FP8 || !SELECTED) ? 1 : 0);
+    // bf16 is loaded into the ring; e4m3 codes into staging tiles, from which
+    // they are converted into the ring
+    static constexpr int CSTAGES = 3;
+    static constexpr int STAGING = FP8 ? CSTAGES * TKEYS * D : 0;
+    // per tile: which keys count, and for e4m3 their scales; selected: rows
     static constexpr int MS = 8;
-    static_assert(2 * MS > STAGES, "meta slots outlive the ring");
-    static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 8 : 0));
-    static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + META + 512;
+    static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 8 : 0) + (SELECTED ? TKEYS * 4 : 0));
+    static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 512;
 };
 
 template <int D, bool FP8, bool SELECTED, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendParams p) {
-    using S = UmmaShape<D, FP8>;
+__global__ void __launch_bounds__(THREADS, 1)
+    attend_umma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                       const AttendParams p) {
+    using S = UmmaShape<D, FP8, SELECTED, SPLIT>;
     constexpr int STAGES = S::STAGES, MS = S::MS;
     constexpr int R = SPLIT ? 128 : 256;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    uint8_t* sQ = smem;                                   // two tiles of 128 rows
-    uint8_t* sT = sQ + 2 * S::TILE;                       // K and V tiles in turn
+    uint8_t* sQ = smem;                                   // tiles of 128 rows
+    uint8_t* sT = sQ + S::QTILES * S::TILE;               // K and V tiles in turn
     uint8_t* sC = sT + STAGES * S::TILE;                  // e4m3 codes on their way
     uint8_t* sM = sC + S::STAGING;
     uint32_t* m_ok = reinterpret_cast<uint32_t*>(sM);     // [MS][4]
-    float* m_lv = reinterpret_cast<float*>(sM + MS * 16); // [MS][4] see log2_above
+    float* m_lv = reinterpret_cast<float*>(sM + MS * 16); // [MS] see log2_above
     float* m_ks = m_lv + MS * 4;                          // [MS][128]
     float* m_vs = m_ks + MS * TKEYS;
+    int* m_row = reinterpret_cast<int*>(FP8 ? m_vs + MS * TKEYS : m_lv);   // [MS][128] token rows
     uint64_t* bars = reinterpret_cast<uint64_t*>(sM + S::META);
     uint64_t* full = bars;                                // [STAGES] tile there
     uint64_t* empty = full + STAGES;                      // [STAGES] tile read
     uint64_t* mfull = empty + STAGES;                     // [MS] meta there
-    uint64_t* sfull = mfull + MS;                         // [2] S there
-    uint64_t* pfull = sfull + 2;                          // [2] P there
-    uint64_t* ofull = pfull + 2;                          // [2] O complete
+    uint64_t* mempty = mfull + MS;                        // [MS] meta read
+    uint64_t* sfull = mempty + MS;                        // [2] S there
+    uint64_t* pfull = sfull + 2;                          // [2][2] half of P there
+    uint64_t* ofull = pfull + 4;                          // [2] O complete
     uint64_t* qfull = ofull + 2;                          // Q there
     uint64_t* drain = qfull + 1;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* cfull = drain + 1;                          // [CSTAGES] codes there
+    uint64_t* cempty = cfull + S::CSTAGES;                // [CSTAGES] codes converted
+    uint64_t* raw = cempty + S::CSTAGES;                  // V tile to be mended there
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(raw + 1);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], FP8 || SELECTED ? 2 : 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < MS; ++i) mbar_init(&mfull[i], 1);
+        for (int i = 0; i < S::CSTAGES; ++i) {
+            mbar_init(&cfull[i], 1);
+            mbar_init(&cempty[i], 2);
+        }
+        for (int i = 0; i < MS; ++i) {
+            mbar_init(&mfull[i], 1);
+            mbar_init(&mempty[i], SPLIT ? 4 : 8);
+        }
+        mbar_init(raw, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
+            mbar_init(&pfull[2 * i], 4);
+            mbar_init(&pfull[2 * i + 1], 4);
             mbar_init(&ofull[i], 1);
         }
         mbar_init(qfull, SPLIT ? 4 : 8);
         mbar_init(drain, 1);
         fence_barrier_init();
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
     }
     if (warp == MMA_WARP) {
         tmem_alloc(tmem_at, 512);
@@ -162,19 +261,21 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
     const long long u_begin = run_begin(units, blockIdx.x, p.ncta);
     const long long u_end = run_begin(units, blockIdx.x + 1, p.ncta);
 
-    if (warp >= LOAD_WARP && warp < MMA_WARP) {
-        // ------------------------------------------------------------- loads
-        // The K and V tiles are numbered in the order of the ring; warp w
-        // takes every third.  A lane looks after keys lane, lane + 32, ... of
-        // its tile: their positions are read two own tiles ahead, their page
-        // ids one.
-        const int lw = warp - LOAD_WARP;
-        long long entry0 = 0;            // tiles of the items before
-        int tile_no = 0;                 // key tiles of the items before
+    if (warp == LOAD_WARP) {
+        // ------------------------------------------------------- rows, loads
+        // A lane looks after keys 4 lane .. 4 lane + 3 of a tile: their
+        // positions are read two tiles ahead, their pages one.  The tile's
+        // token rows, scales and which keys count go to shared memory.  Paged:
+        // this warp then loads the tile, a page (or 128 keys of it) a TMA box.
         bool aborted = false;
-        constexpr int CH = D * (FP8 ? 1 : 2) / 16;         // 16-byte chunks of a stored row
-        constexpr int KPI = 32 / CH;                       // keys an instruction
-        const int ch = lane % CH, sub = lane / CH;
+        uint32_t ms = 0, mph = 1;        // next meta slot, and the phase of its release
+        uint32_t slot = 0, ph = 1;       // the same of the ring (e4m3: of the staging tiles)
+        uint32_t loaded = 0, raws = 0;   // tiles issued so far; loads mended before use
+        uint64_t* there = FP8 ? cfull : full;
+        uint64_t* read = FP8 ? cempty : empty;
+        constexpr uint32_t RING = FP8 ? S::CSTAGES : STAGES;
+        const int box = min(TKEYS, p.c.page_size());           // keys of a TMA box
+        const int boxes = TKEYS / box;
         for (long long u = u_begin; u < u_end && !aborted;) {
             const Item it = find_item<SELECTED>(p, u);
             const int ta = it.tile0 + (int)(u - it.unit0);
@@ -186,175 +287,313 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
             const int key_lo = p.window ? max(0, lim_lo - p.window + 1) : 0;
             const int32_t* sel = SELECTED ? p.idx + (size_t)it.first * p.topk : nullptr;
             const int32_t* pages = p.c.table + (size_t)it.b * p.c.max_pages;
-            const size_t head_off = (size_t)it.h * D * (FP8 ? 1 : 2) + ch * 16;
-            const int total = 2 * (tz - ta);               // tiles of this item
-            int x = (int)((lw + 3 - entry0 % 3) % 3);      // the next one of this warp
-            auto position = [&](int x, int g) -> int {
-                const int t = ta + (x >> 1), s = t * TKEYS + g * 32 + lane;
-                if (x >= total) return -1;
+            // selected: a key that does not count is replaced by the token's
+            // own, so that V holds nothing but finite numbers
+            const int spare = SELECTED ? max(p.c.row_of(pages[lim_hi >> p.c.page_log2], lim_hi), 0) : 0;
+            auto position = [&](int t, int i) -> int {
+                const int s = t * TKEYS + 4 * lane + i;
+                if (t >= tz) return -1;
                 if constexpr (SELECTED) return s < p.topk ? ld_nc_early(sel + s) : -1;
-                else return s >= key_lo && s <= lim_hi ? s : -1;
+                else return s;
             };
-            auto page_of = [&](int pos) -> int {
-                if (SELECTED && pos > it.pos0) return -2;
-                return pos >= 0 ? ld_nc_early(pages + (pos >> p.c.page_log2)) : -2;
-            };
+            auto counts = [&](int pos) { return pos >= key_lo && pos <= lim_hi; };
             int pos_a[4], page_a[4], pos_b[4];
+            auto pages_of = [&]() {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) pos_a[g] = position(x, g);
+                for (int i = 0; i < 4; ++i)
+                    page_a[i] = counts(pos_a[i]) ? ld_nc_early(pages + (pos_a[i] >> p.c.page_log2)) : -1;
+            };
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                page_a[g] = page_of(pos_a[g]);
-                pos_b[g] = position(x + 3, g);
+            for (int i = 0; i < 4; ++i) {
+                pos_a[i] = position(ta, i);
+                pos_b[i] = position(ta + 1, i);
             }
-            // Token rows of this lane's keys of tile x; the next own tile's
-            // pages and the positions after it are then under way.  All waits
-            // come before all loads: a load waited for beside younger ones
-            // costs their latency too.
-            auto resolve = [&](int x, int (&row)[4]) {
+            pages_of();
+            for (int t = ta; t < tz && !aborted; ++t) {
+                // all waits for loads come before the next loads: one waited
+                // for beside younger ones costs their latency too
+                int row[4];
+                // keys of a lane lie on one page; -1 where one does not count
+                const int my_page = max(max(page_a[0], page_a[1]), max(page_a[2], page_a[3]));
+                uint32_t ok = 0;
+                float ks[4], vs[4];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    row[g] = -1;
-                    if (page_a[g] != -2) {
-                        row[g] = p.c.row_of(page_a[g], pos_a[g]);
-                        if (row[g] < 0) raise_error(ERRBIT_DATA);
+                for (int i = 0; i < 4; ++i) {
+                    row[i] = -1;
+                    if (counts(pos_a[i])) {
+                        row[i] = p.c.row_of(page_a[i], pos_a[i]);
+                        if (row[i] < 0) raise_error(ERRBIT_DATA);
                     }
-                    pos_a[g] = pos_b[g];
+                    ok |= (row[i] >= 0 ? 1u : 0u) << i;
+                    pos_a[i] = pos_b[i];
                 }
+                if constexpr (FP8) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) page_a[g] = page_of(pos_a[g]);
+                    for (int i = 0; i < 4; ++i) {
+                        ks[i] = row[i] >= 0 ? ld_nc_early(p.c.ks + row[i]) : 0.0f;
+                        vs[i] = row[i] >= 0 ? ld_nc_early(p.c.vs + row[i]) : 0.0f;
+                    }
+                }
+                pages_of();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) pos_b[g] = position(x + 6, g);
-            };
-            auto wait_slot = [&](long long e) -> bool {
-                return __all_sync(0xffffffffu, mbar_wait(&empty[e % STAGES], (uint32_t)((e / STAGES) & 1) ^ 1));
-            };
-            auto publish = [&](long long e) {
-                fence_proxy_async_smem();
+                for (int i = 0; i < 4; ++i) pos_b[i] = position(t + 2, i);
+                const uint32_t mine = ok;
+                ok <<= 4 * (lane & 7);                         // eight lanes make a word
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) ok |= __shfl_xor_sync(0xffffffffu, ok, d);
+                if (!__all_sync(0xffffffffu, mbar_wait(&mempty[ms], mph))) {
+                    aborted = true;
+                    break;
+                }
+                if ((lane & 7) == 0) m_ok[ms * 4 + (lane >> 3)] = ok;
+                if constexpr (SELECTED)
+                    *reinterpret_cast<int4*>(m_row + ms * TKEYS + 4 * lane) =
+                        make_int4(row[0] >= 0 ? row[0] : spare, row[1] >= 0 ? row[1] : spare,
+                                  row[2] >= 0 ? row[2] : spare, row[3] >= 0 ? row[3] : spare);
+                if constexpr (FP8) {
+                    const float lv = log2_above(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
+                                                      fmaxf(fabsf(vs[2]), fabsf(vs[3]))));
+                    if (lane == 0) m_lv[ms] = lv;
+                    *reinterpret_cast<float4*>(m_ks + ms * TKEYS + 4 * lane) =
+                        make_float4(ks[0], ks[1], ks[2], ks[3]);
+                    *reinterpret_cast<float4*>(m_vs + ms * TKEYS + 4 * lane) =
+                        make_float4(vs[0], vs[1], vs[2], vs[3]);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[e % STAGES]);
-            };
-            if constexpr (!FP8) {
-                for (; x < total; x += 3) {
-                    const long long e = entry0 + x;
-                    int row[4];
-                    uint32_t ok[4];
-                    resolve(x, row);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) ok[g] = __ballot_sync(0xffffffffu, row[g] >= 0);
-                    if (!wait_slot(e)) { aborted = true; break; }
-                    if ((x & 1) == 0 && lane < 4)
-                        m_ok[((tile_no + (x >> 1)) % MS) * 4 + lane] =
-                            lane == 0 ? ok[0] : lane == 1 ? ok[1] : lane == 2 ? ok[2] : ok[3];
-                    const uint8_t* plane = ((x & 1) ? p.c.v : p.c.k) + head_off;
-                    const uint32_t dst = smem_u32(sT + (e % STAGES) * S::TILE) + (ch >> 3) * (TKEYS * 128);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int i = 0; i < 32 / KPI; ++i) {
-                            const int kr = i * KPI + sub;
-                            const int r = __shfl_sync(0xffffffffu, row[g], kr);
-                            cp16_or_zero(dst + sw128_offset(g * 32 + kr, ch & 7),
-                                         plane + (size_t)(r < 0 ? 0 : r) * p.c.rowb, r >= 0);
-                        }
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    publish(e);
+                if (lane == 0) mbar_arrive(&mfull[ms]);
+                if (++ms == MS) {
+                    ms = 0;
+                    mph ^= 1;
                 }
-            } else {
-                // Codes are copied to a staging tile of the warp, 32 keys at a
-                // time, and converted from there; the space of 32 converted
-                // keys takes the same keys of the warp's next tile at once.  A
-                // lane converts the chunks that it copied itself.
-                const uint32_t mine = smem_u32(sC) + lw * (TKEYS * D) + lane * 16;
-                int row[4];                                // of the tile being copied
-                float ks[4], vs[4], ks_n[4], vs_n[4];      // of the tile in staging, and of the next
-                uint32_t ok[4], ok_n[4];
-                auto look_up = [&](int x) {
-                    if (x >= total) return;
-                    resolve(x, row);
+                if constexpr (!SELECTED) {
+                    // lane i loads box i (of 64-value half i / boxes); a box
+                    // with no key that counts is left out
+                    const int part = lane % boxes, half = lane / boxes;
+                    constexpr int HALVES = FP8 ? 1 : D / 64;
+                    const int from = part * box / 4;           // the lane of the box's first keys
+                    const uint32_t any = __ballot_sync(0xffffffffu, mine != 0);
+                    const uint32_t its = box == TKEYS ? any : (any >> from) & ((1u << (box / 4)) - 1);
+                    const int page = __shfl_sync(0xffffffffu, my_page, its ? from + __ffs(its) - 1 : 0);
+                    const int at = (page << p.c.page_log2) + ((t * TKEYS + part * box) & (p.c.page_size() - 1));
+                    const bool go = half < HALVES && its != 0;
+                    const uint32_t bytes =
+                        __popc(__ballot_sync(0xffffffffu, go)) * box * (FP8 ? D : 128);
+                    const bool every = __all_sync(0xffffffffu, mine == 15u);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        ok_n[g] = __ballot_sync(0xffffffffu, row[g] >= 0);
-                        ks_n[g] = vs_n[g] = 0.0f;
-                        if ((x & 1) == 0 && row[g] >= 0) {
-                            ks_n[g] = ld_nc_early(p.c.ks + row[g]);
-                            vs_n[g] = ld_nc_early(p.c.vs + row[g]);
+                    for (int kv = 0; kv < 2 && !aborted; ++kv) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(&read[slot], ph))) {
+                            aborted = true;
+                            break;
                         }
-                    }
-                };
-                auto load = [&](int x, int g) {
-                    if (x < total) {
-                        const uint8_t* plane = ((x & 1) ? p.c.v : p.c.k) + head_off;
-#pragma unroll
-                        for (int i = 0; i < 32 / KPI; ++i) {
-                            const int r = __shfl_sync(0xffffffffu, row[g], i * KPI + sub);
-                            cp16_or_zero(mine + g * (32 * D) + i * 512,
-                                         plane + (size_t)(r < 0 ? 0 : r) * p.c.rowb, r >= 0);
+                        // bf16 values of keys that do not count are zeroed
+                        // before use (e4m3: by the converting warps)
+                        const bool mend = !FP8 && kv && !every;
+                        uint64_t* bar = mend ? raw : &there[slot];
+                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                        __syncwarp();
+                        if (go) {
+                            if constexpr (FP8)
+                                tma_load_2d(sC + slot * (TKEYS * D) + part * box * D, kv ? &tmap_v : &tmap_k, bar,
+                                            it.h * D, at);
+                            else
+                                tma_load_2d(sT + slot * S::TILE + half * (TKEYS * 128) + part * box * 128,
+                                            kv ? &tmap_v : &tmap_k, bar, it.h * D + half * 64, at);
                         }
-                    }
-                    cp_async_commit();
-                };
-                look_up(x);
+                        if (mend) {
+                            if (!__all_sync(0xffffffffu, mbar_wait(raw, raws & 1))) aborted = true;
+                            ++raws;
+                            const uint32_t base = smem_u32(sT + slot * S::TILE);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) load(x, g);
-                for (; x < total; x += 3) {
-                    const long long e = entry0 + x;
-                    if (!wait_slot(e)) { aborted = true; break; }
-                    const int ms = (tile_no + (x >> 1)) % MS;
-                    const uint32_t dst = smem_u32(sT + (e % STAGES) * S::TILE) + (ch >> 2) * (TKEYS * 128);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) { ks[g] = ks_n[g]; vs[g] = vs_n[g]; ok[g] = ok_n[g]; }
-                    look_up(x + 3);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        cp_async_wait<3>();
-                        if ((x & 1) == 0) {
-                            const float lv = log2_above(vs[g]);
-                            if (lane == 0) {
-                                m_ok[ms * 4 + g] = ok[g];
-                                m_lv[ms * 4 + g] = lv;
+                            for (int i = 0; i < 4; ++i) {
+                                if ((mine >> i) & 1) continue;
+                                const int k = 4 * lane + i;
+                                for (int c = 0; c < D / 8; ++c)
+                                    sts16(base + (c >> 3) * (TKEYS * 128) + k * 128 + (c & 7) * 16, 0, 0, 0, 0);
                             }
-                            m_ks[ms * TKEYS + g * 32 + lane] = ks[g];
-                            m_vs[ms * TKEYS + g * 32 + lane] = vs[g];
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&full[slot]);
                         }
-                        // all of the group's reads come first: stores between
-                        // them would hold each up behind the last one's chain
-                        uint4 w[32 / KPI];
-#pragma unroll
-                        for (int i = 0; i < 32 / KPI; ++i)
-                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                                         : "r"(mine + g * (32 * D) + i * 512)
-                                         : "memory");
-#pragma unroll
-                        for (int i = 0; i < 32 / KPI; ++i) {
-                            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                            uint32_t y[8];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                y[2 * k] = e4m3x2_f16x2((uint16_t)(v[k] & 0xFFFFu));
-                                y[2 * k + 1] = e4m3x2_f16x2((uint16_t)(v[k] >> 16));
-                            }
-                            const int r = g * 32 + i * KPI + sub, c0 = 2 * (ch & 3);
-                            // the upper 64 values' lanes write their second half
-                            // first: the eight lanes of a row cover all banks
-                            const int s = ch >> 2;
-                            const uint32_t d0 = dst + sw128_offset(r, c0 + s);
-                            const uint32_t d1 = dst + sw128_offset(r, c0 + 1 - s);
-                            sts16(d0, s ? y[4] : y[0], s ? y[5] : y[1], s ? y[6] : y[2], s ? y[7] : y[3]);
-                            sts16(d1, s ? y[0] : y[4], s ? y[1] : y[5], s ? y[2] : y[6], s ? y[3] : y[7]);
+                        ++loaded;
+                        if (++slot == RING) {
+                            slot = 0;
+                            ph ^= 1;
                         }
-                        load(x + 3, g);
                     }
-                    publish(e);
                 }
-                cp_async_wait<0>();
             }
-            entry0 += total;
-            tile_no += tz - ta;
         }
-        cp_async_wait<0>();
+        // every load has landed before the CTA may end
+        for (uint32_t i = 0; i < RING && i < loaded; ++i) {
+            const uint32_t e = loaded - 1 - i;
+            mbar_wait(&there[e % RING], (e / RING) & 1);
+        }
+    } else if (warp > LOAD_WARP && warp < MMA_WARP) {
+        // ------------------- selected keys; e4m3 codes to halves (exact)
+        // Two warps, 64 keys of each tile each.  Selected keys are copied
+        // row by row: bf16 into the ring, codes into the staging tiles.
+        if constexpr (FP8 || SELECTED) {
+            const int w64 = (warp - LOAD_WARP - 1) * 64;
+            bool aborted = false;
+            uint32_t ms = 0, mph = 0;              // meta of the next tile to copy (or convert)
+            uint32_t cs = 0, cph = 0;              // staging tile to convert
+            uint32_t slot = 0, ph = 1;             // ring slot to fill
+            const int es = FP8 ? 1 : 2;
+            // e4m3: eight neighbouring lanes take four chunks of two keys
+            // whose numbers differ in bits 0 and 2 (D = 64: in bit 0): their
+            // reads of codes and writes of halves fall on different banks
+            constexpr int CH = D * (FP8 ? 1 : 2) / 16;         // 16-byte chunks of a stored row
+            constexpr int KPI = 32 / CH;                       // keys an instruction
+            const int ch = !FP8 ? lane % CH : (lane & 3) | (D == 128 ? (lane >> 4) << 2 : 0);
+            auto key_of = [&](int j) -> int {                  // of instruction j
+                if constexpr (FP8 && D == 128) {
+                    const int q = (lane >> 2) & 3;
+                    return w64 + (j >> 1) * 8 + (((j & 1) * 2 + (q >> 1)) ^ ((q & 1) * 5));
+                } else if constexpr (FP8) {
+                    return w64 + j * 8 + (lane >> 2);
+                } else {
+                    return w64 + j * KPI + lane / CH;
+                }
+            };
+            auto code_at = [&](uint32_t stage, int k) -> uint32_t {
+                return smem_u32(sC) + stage * (TKEYS * D) +
+                       (D == 128 ? k * 128 + ((ch ^ (k & 7)) << 4) : k * 64 + ch * 16);
+            };
+            auto advance = [](uint32_t& at, uint32_t& phase, uint32_t n) {
+                if (++at == n) {
+                    at = 0;
+                    phase ^= 1;
+                }
+            };
+            for (long long u = u_begin; u < u_end && !aborted;) {
+                const Item it = find_item<SELECTED>(p, u);
+                const int ta = it.tile0 + (int)(u - it.unit0);
+                const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
+                u = it.unit0 + (tz - it.tile0);
+                if (!it.ok) continue;
+                const int total = 2 * (tz - ta);               // K and V tiles of the item
+                const size_t head_off = (size_t)it.h * D * es + ch * 16;
+                // copies of tile x (K if even) towards shared memory at dst(k)
+                auto copy = [&](int x, auto dst) -> bool {
+                    if ((x & 1) == 0 && !__all_sync(0xffffffffu, mbar_wait(&mfull[ms], mph))) return false;
+                    const uint8_t* plane = ((x & 1) ? p.c.v : p.c.k) + head_off;
+#pragma unroll
+                    for (int j = 0; j < 64 / KPI; ++j) {
+                        const int k = key_of(j);
+                        cp_async16(dst(k), plane + (size_t)m_row[ms * TKEYS + k] * p.c.rowb);
+                    }
+                    if (x & 1) advance(ms, mph, MS);
+                    return true;
+                };
+                auto publish = [&](uint32_t at) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[at]);
+                };
+                if constexpr (!FP8) {
+                    // up to three tiles in flight; a slot is released once
+                    // the tile after its own is published at the latest, so
+                    // waiting for one with STAGES - 3 unpublished is safe
+                    constexpr int PENDING = STAGES >= 5 ? 2 : 1;
+                    uint32_t pend[PENDING];
+                    int npend = 0;
+                    for (int x = 0; x < total && !aborted; ++x) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph))) aborted = true;
+                        const uint32_t base = smem_u32(sT) + slot * S::TILE + (ch >> 3) * (TKEYS * 128);
+                        if (!aborted && !copy(x, [&](int k) { return base + sw128_offset(k, ch & 7); }))
+                            aborted = true;
+                        cp_async_commit();
+                        if (npend == PENDING) {
+                            cp_async_wait<PENDING>();
+                            publish(pend[0]);
+#pragma unroll
+                            for (int i = 0; i + 1 < PENDING; ++i) pend[i] = pend[i + 1];
+                            --npend;
+                        }
+#pragma unroll
+                        for (int i = 0; i < PENDING; ++i)
+                            if (i == npend) pend[i] = slot;
+                        ++npend;
+                        advance(slot, ph, STAGES);
+                    }
+                    cp_async_wait<0>();
+#pragma unroll
+                    for (int i = 0; i < PENDING; ++i)
+                        if (i < npend) publish(pend[i]);
+                } else {
+                    // staging tiles are filled two ahead (selected: by these
+                    // warps themselves, each its own keys)
+                    uint32_t fs = cs;                          // staging tile to fill
+                    auto fill = [&](int x) {
+                        if (SELECTED && x < total && !aborted) {
+                            if (!copy(x, [&](int k) { return code_at(fs, k); })) aborted = true;
+                            if (++fs == S::CSTAGES) fs = 0;
+                        }
+                        if (SELECTED) cp_async_commit();
+                    };
+                    fill(0);
+                    fill(1);
+                    for (int x = 0; x < total; ++x) {
+                        if constexpr (SELECTED) {
+                            cp_async_wait<1>();
+                            __syncwarp();
+                        }
+                        const bool got = (SELECTED || mbar_wait(&cfull[cs], cph)) && mbar_wait(&empty[slot], ph);
+                        if (!__all_sync(0xffffffffu, got && !aborted)) {
+                            aborted = true;
+                            break;
+                        }
+                        uint32_t ok[2] = {0xffffffffu, 0xffffffffu};
+                        if constexpr (!SELECTED) {             // values that do not count: 0
+                            if (x & 1) {
+                                ok[0] = m_ok[ms * 4 + (w64 >> 5)];
+                                ok[1] = m_ok[ms * 4 + (w64 >> 5) + 1];
+                                advance(ms, mph, MS);
+                            }
+                        }
+                        const bool every = (ok[0] & ok[1]) == 0xffffffffu;
+                        const uint32_t dst = smem_u32(sT) + slot * S::TILE + (ch >> 2) * (TKEYS * 128);
+                        constexpr int BATCH = 8;               // reads before the writes
+#pragma unroll
+                        for (int j0 = 0; j0 < 64 / KPI; j0 += BATCH) {
+                            uint4 c[BATCH];
+#pragma unroll
+                            for (int j = 0; j < BATCH; ++j)
+                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(c[j].x), "=r"(c[j].y), "=r"(c[j].z), "=r"(c[j].w)
+                                             : "r"(code_at(cs, key_of(j0 + j)))
+                                             : "memory");
+                            if (!every) {
+#pragma unroll
+                                for (int j = 0; j < BATCH; ++j) {
+                                    const int k = key_of(j0 + j) - w64;
+                                    if (!((ok[k >> 5] >> (k & 31)) & 1)) c[j] = make_uint4(0, 0, 0, 0);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < BATCH; ++j) {
+                                const uint32_t v[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+                                uint32_t y[8];
+#pragma unroll
+                                for (int n = 0; n < 4; ++n) {
+                                    y[2 * n] = e4m3x2_f16x2((uint16_t)(v[n] & 0xFFFFu));
+                                    y[2 * n + 1] = e4m3x2_f16x2((uint16_t)(v[n] >> 16));
+                                }
+                                const int k = key_of(j0 + j), c0 = 2 * (ch & 3);
+                                sts16(dst + sw128_offset(k, c0), y[0], y[1], y[2], y[3]);
+                                sts16(dst + sw128_offset(k, c0 + 1), y[4], y[5], y[6], y[7]);
+                            }
+                        }
+                        publish(slot);
+                        if (!SELECTED && lane == 0) mbar_arrive(&cempty[cs]);
+                        advance(cs, cph, S::CSTAGES);
+                        advance(slot, ph, STAGES);
+                        fill(x + 2);
+                    }
+                }
+            }
+            cp_async_wait<0>();
+        }
     } else if (warp == MMA_WARP) {
         // ------------------------------------------------------------- MMA
         // The whole warp walks the steps and one lane issues: descriptors
@@ -367,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
         const uint64_t dk = smem_desc_k_sw128(smem_u32(sT)), dv = smem_desc_mn_sw128(smem_u32(sT));
         constexpr uint32_t TILE16 = S::TILE >> 4;      // descriptor addresses count 16 bytes
         // ring positions of the next K and V tiles, and their phases
-        uint32_t ks = 0, kph = 0, vs = 1, vph = 0, ms = 0;
+        uint32_t ks = 0, kph = 0, vs = 1, vph = 0;
         auto next = [](uint32_t& slot, uint32_t& ph) {
             slot += 2;
             if (slot >= STAGES) {
@@ -383,8 +622,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
             if (SPLIT || t == 0) {
                 if (!mbar_wait(&full[ks], kph)) return false;
                 tc_fence_after();
-                if (leader) mbar_arrive(&mfull[ms]);
-                ms = (ms + 1) % MS;
             }
             if (leader) {
                 const uint64_t a = dq + (SPLIT ? 0 : t * TILE16), b = dk + ks * TILE16;
@@ -412,16 +649,22 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
             tc_fence_after();
             aborted = !do_s(0) || (H > 1 && !do_s(1));
             auto step = [&](int h, int t) -> bool {
-                if (!mbar_wait(&pfull[t], pph[t])) return false;
-                pph[t] ^= 1;
                 if ((SPLIT || t == 0) && !mbar_wait(&full[vs], vph)) return false;
-                tc_fence_after();
-                if (leader) {
-                    const uint64_t b = dv + vs * TILE16;
+                const uint64_t b = dv + vs * TILE16;
 #pragma unroll
-                    for (int i = 0; i < TKEYS / 16; ++i)
-                        umma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, b + i * (2048 >> 4), id_o,
-                                i > 0 ? 1u : (uint32_t)(h > 1));
+                for (int half = 0; half < 2; ++half) {
+                    if (!mbar_wait(&pfull[2 * t + half], pph[t])) return false;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int i = 4 * half; i < 4 * half + 4; ++i)
+                            umma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, b + i * (2048 >> 4),
+                                    id_o, i > 0 ? 1u : (uint32_t)(h > 1));
+                    }
+                    __syncwarp();
+                }
+                pph[t] ^= 1;
+                if (leader) {
                     if (SPLIT || t == 1) umma_commit(&empty[vs]);
                     if (h + 2 >= H) umma_commit(&ofull[t]);
                 }
@@ -440,42 +683,56 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
     } else {
         // --------------------------------------------------------- softmax
         const int t = warp >> 2;
-        const int r = (threadIdx.x & 127);                 // row of the tile, TMEM lane
+        const int r = (warp & 3) * 32 + lane;              // row of the tile, TMEM lane
         const int rb = SPLIT ? r : t * 128 + r;            // row of the block
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + 256 + t * 128;
-        uint32_t steps = 0, ends = 0;
+        const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + 256;
+        constexpr bool NEEDS_Q1 = !SPLIT || FP8;           // the odd tiles' threads need their row
+        uint32_t sph = 0, oph[2] = {0, 0};
         int tile_no = 0;
         bool aborted = false;
-        for (long long u = u_begin; u < u_end;) {
-            const Item it = find_item<SELECTED>(p, u);
-            const int ta = it.tile0 + (int)(u - it.unit0);
-            const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
-            const bool whole = it.unit0 >= u_begin && it.unit0 + it.tiles <= u_end;
-            const int slot = 2 * blockIdx.x + (it.unit0 < u_begin ? 0 : 1);
-            u = it.unit0 + (tz - it.tile0);
-            if (!it.ok) continue;
-            const int n = tz - ta;
-            const bool live = rb < it.rows;
-            const int rr = it.row0 + rb;
-            const size_t head = live ? (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G : 0;
-            const int lim = live ? it.pos0 + rr / p.G : -1;
-            const int lim_lo = it.pos0 + it.row0 / p.G;
-            const int lim_hi = it.pos0 + (it.row0 + it.rows - 1) / p.G;
 
+        // the run's items in turn; the next one and its query row are read
+        // while the last product of the one before is under way
+        long long u = u_begin;
+        Item it;
+        int ta, tz, slot;
+        bool whole, live;
+        size_t head;
+        uint4 qrow[D / 8];
+        auto fetch = [&]() -> bool {
+            while (u < u_end) {
+                it = find_item<SELECTED>(p, u);
+                ta = it.tile0 + (int)(u - it.unit0);
+                tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
+                whole = it.unit0 >= u_begin && it.unit0 + it.tiles <= u_end;
+                slot = 2 * blockIdx.x + (it.unit0 < u_begin ? 0 : 1);
+                u = it.unit0 + (tz - it.tile0);
+                if (!it.ok) continue;
+                live = rb < it.rows;
+                const int rr = it.row0 + rb;
+                head = live ? (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G : 0;
+                if (NEEDS_Q1 || t == 0) {
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + head * D);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) qrow[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                }
+                return true;
+            }
+            return false;
+        };
+        bool more = fetch();
+        while (more) {
             // ---- this thread's query row into the swizzled tile (for e4m3
             // as halves, divided by the power of two under its largest value)
             float c = p.scale_log2;
-            if (!SPLIT || t == 0) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + head * D);
-                const uint32_t dst = smem_u32(sQ) + t * S::TILE;
+            if (NEEDS_Q1 || t == 0) {
                 float down = 1.0f;
                 if constexpr (FP8) {
                     float amax = 0.0f;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
-                        const uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        const uint32_t w[4] = {qrow[i].x, qrow[i].y, qrow[i].z, qrow[i].w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
@@ -487,37 +744,28 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                         down = __uint_as_float(0x7F000000u - e);
                     }
                 }
+                if (!SPLIT || t == 0) {
+                    const uint32_t dst = smem_u32(sQ) + (SPLIT ? 0 : t * S::TILE);
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    if constexpr (FP8) {
-                        uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
+                    for (int i = 0; i < D / 8; ++i) {
+                        uint32_t w[4] = {qrow[i].x, qrow[i].y, qrow[i].z, qrow[i].w};
+                        if constexpr (FP8) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *w[k] = f16x2(__uint_as_float(*w[k] << 16) * down,
-                                          __uint_as_float(*w[k] & 0xFFFF0000u) * down);
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = f16x2(__uint_as_float(w[k] << 16) * down,
+                                             __uint_as_float(w[k] & 0xFFFF0000u) * down);
+                        }
+                        sts16(dst + (i >> 3) * (TKEYS * 128) + sw128_offset(r, i & 7), w[0], w[1], w[2], w[3]);
                     }
-                    sts16(dst + (i >> 3) * (TKEYS * 128) + sw128_offset(r, i & 7), x.x, x.y, x.z, x.w);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(qfull);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(qfull);
-            } else if constexpr (FP8) {
-                // the odd tiles' threads need the row's factor only
-                float amax = 0.0f;
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + head * D);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
-                                                 fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
-                }
-                const uint32_t e = __float_as_uint(amax) & 0x7F800000u;
-                if (e > 0x01000000u && e < 0x7E000000u) c *= __uint_as_float(e);
             }
+            const int n = tz - ta;
+            const int lim = live ? it.pos0 + (it.row0 + rb) / p.G : -1;
+            const int lim_lo = it.pos0 + it.row0 / p.G;
+            const int lim_hi = it.pos0 + (it.row0 + it.rows - 1) / p.G;
 
             float m = -INFINITY, l = 0.0f;
             bool begun = false;                            // O holds sums
@@ -525,10 +773,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                 const int ms = (tile_no + j) % MS;
                 const uint32_t mph = (uint32_t)(((tile_no + j) / MS) & 1);
                 if (!aborted) {
-                    const bool got = mbar_wait(&sfull[t], steps & 1) && mbar_wait(&mfull[ms], mph);
+                    const bool got = mbar_wait(&sfull[t], sph) && mbar_wait(&mfull[ms], mph);
                     if (!__all_sync(0xffffffffu, got)) aborted = true;
                 }
-                ++steps;
+                sph ^= 1;
                 if (aborted) continue;
                 tc_fence_after();
                 float s[TKEYS];
@@ -551,27 +799,29 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                 if (!plain) {
                     const uint32_t ok[4] = {okv.x, okv.y, okv.z, okv.w};
                     // keys from..to of the tile are this row's
-                    const int to = SELECTED ? TKEYS - 1 : lim - key0;
-                    const int from = !SELECTED && p.window ? lim - p.window + 1 - key0 : 0;
+                    const int to = SELECTED ? TKEYS - 1 : min(lim - key0, TKEYS - 1);
+                    const int from = !SELECTED && p.window ? max(lim - p.window + 1 - key0, 0) : 0;
 #pragma unroll
-                    for (int k = 0; k < TKEYS; ++k) {
-                        const bool see = ((ok[k >> 5] >> (k & 31)) & 1) && k <= to && k >= from;
-                        s[k] = see ? s[k] : -INFINITY;
+                    for (int i = 0; i < 4; ++i) {
+                        const int a = min(max(from - 32 * i, 0), 32), z = min(max(to - 32 * i + 1, 0), 32);
+                        const uint32_t below = z == 32 ? 0xffffffffu : (1u << z) - 1;
+                        const uint32_t above = a == 32 ? 0u : 0xffffffffu << a;
+                        const uint32_t see = ok[i] & below & above;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            s[32 * i + k] = (see >> k) & 1 ? s[32 * i + k] : -INFINITY;
                     }
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int k = 4; k < TKEYS; k += 4) {
-                    mx[0] = fmaxf(mx[0], s[k]);
-                    mx[1] = fmaxf(mx[1], s[k + 1]);
-                    mx[2] = fmaxf(mx[2], s[k + 2]);
-                    mx[3] = fmaxf(mx[3], s[k + 3]);
+                for (int k = 4; k < TKEYS - 4; k += 8) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[k + y], s[k + 4 + y]);
                 }
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                if constexpr (FP8) {
-                    const float4 lv = *reinterpret_cast<const float4*>(m_lv + ms * 4);
-                    top += fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
-                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[TKEYS - 4 + y]);
+                float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+                if constexpr (FP8) top += m_lv[ms];
                 // The reference point m may lag behind the maximum by up to
                 // 8: weights then reach 2^8, which costs no precision, and
                 // the sums in TMEM seldom have to be multiplied.  For e4m3
@@ -589,131 +839,105 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
 #pragma unroll 1
                     for (int i = 0; i < D / 16; ++i) {
                         uint32_t o[16];
-                        asm volatile(
-                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]),
-                              "=r"(o[6]), "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]),
-                              "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                            : "r"(tO + i * 16));
+                        tmem_ld16(tO + t * 128 + i * 16, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st16(tO + i * 16, o);
+                        tmem_st16(tO + t * 128 + i * 16, o);
                     }
+                    tmem_st_wait();
                 }
                 begun = true;
                 const float z = m == -INFINITY ? 0.0f : -m;
-                const uint64_t c2 = pack2(c, c), z2 = pack2(z, z);
-                const float4* vs = reinterpret_cast<const float4*>(m_vs + ms * TKEYS);
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float* vs = m_vs + ms * TKEYS;
+                // the product with V starts on the first 64 keys' weights
+                // while the others' are computed
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        float* x = s + i * 32 + k;
-                        float e[4];
-                        unpack2(ffma2(pack2(x[0], x[1]), c2, z2), e[0], e[1]);
-                        unpack2(ffma2(pack2(x[2], x[3]), c2, z2), e[2], e[3]);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            e[y] = ex2(e[y]);
-                            sum[y] += e[y];
-                        }
-                        if constexpr (FP8) {
-                            const float4 v = vs[(i * 32 + k) / 4];
-                            e[0] *= v.x; e[1] *= v.y; e[2] *= v.z; e[3] *= v.w;
-                        }
-                        pk[k / 2] = FP8 ? f16x2(e[0], e[1]) : bf16x2(e[0], e[1]);
-                        pk[k / 2 + 1] = FP8 ? f16x2(e[2], e[3]) : bf16x2(e[2], e[3]);
-                    }
-                    tmem_st16(tS + i * 16, pk);
+                for (int i = 0; i < 2; ++i) {
+                    l += plain ? weights<FP8, true>(s + i * 64, c, z, vs + i * 64, tS + i * 32)
+                               : weights<FP8, false>(s + i * 64, c, z, vs + i * 64, tS + i * 32);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[2 * t + i]);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[t]);
+                if (lane == 0) mbar_arrive(&mempty[ms]);
             }
             tile_no += n;
 
-            // ---- the item's end: O is complete
-            if (n > (SPLIT ? t : 0)) {
-                if (!aborted) {
-                    const bool got = mbar_wait(&ofull[t], ends & 1);
-                    if (!__all_sync(0xffffffffu, got)) aborted = true;
+            // ---- the item's end
+            const bool out_whole = whole, out_live = live;
+            const size_t out_head = head;
+            float* part = p.part + (size_t)slot * slot_words(R, D);
+            more = fetch();
+            if (!aborted) {
+                bool got = true;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    if ((SPLIT || y == t) && n > (SPLIT ? y : 0)) {
+                        got = got && mbar_wait(&ofull[y], oph[y]);
+                        oph[y] ^= 1;
+                    }
                 }
-                ++ends;
+                if (!__all_sync(0xffffffffu, got)) aborted = true;
             }
             tc_fence_after();
-            float f0 = 1.0f, f1 = 0.0f;
-            float* other = reinterpret_cast<float*>(sQ);       // SPLIT: tile 1's sums, [128][D]
+            float f0 = 1.0f, f1 = 0.0f;                    // of tile 0's and 1's sums
             if constexpr (SPLIT) {
-                // the odd tiles' sums go through the query rows' memory, which
-                // the last product has left: both halves wait for each other
-                __shared__ float ml[2][128];
+                // both halves' threads of a row join the sums of the even and
+                // odd tiles, half of the values each (TMEM lanes belong to
+                // warps by their number modulo 4, so both can read both)
+                // columns of S that P leaves free carry the statistics over
+                tmem_st2(tS + 64, __float_as_uint(m), __float_as_uint(l));
+                tmem_st_wait();
+                tc_fence_before();
                 named_bar_sync(1, 256);
-                if (t == 1) {
-                    ml[0][r] = m;
-                    ml[1][r] = l;
-                    if (begun && !aborted) {
+                tc_fence_after();
+                uint32_t om, ol;
+                tmem_ld2(tmem + lane_off + (t ^ 1) * 128 + 64, om, ol);
+                tmem_ld_wait();
+                const float mt[2] = {t ? __uint_as_float(om) : m, t ? m : __uint_as_float(om)};
+                const float lt[2] = {t ? __uint_as_float(ol) : l, t ? l : __uint_as_float(ol)};
+                m = fmaxf(mt[0], mt[1]);                   // tile 1 without keys: -inf, 0
+                const float zz = m == -INFINITY ? 0.0f : m;
+                f0 = ex2(mt[0] - zz);
+                f1 = ex2(mt[1] - zz);
+                l = lt[0] * f0 + lt[1] * f1;
+            }
+            if (!aborted) {
+                const bool none = m == -INFINITY && l == 0.0f;
+                const float inv = out_whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
+                constexpr int PARTS = SPLIT ? D / 64 : D / 32;     // 32 values each
+                const int first = SPLIT ? t * PARTS : 0;
+                f0 *= inv;
+                f1 *= inv;
 #pragma unroll 1
-                        for (int i = 0; i < D / 32; ++i) {
-                            float o[32];
-                            tmem_ld32(tO + i * 32, o);
+                for (int i = first; i < first + PARTS; ++i) {
+                    float o[32];
+                    tmem_ld32(tO + (SPLIT ? 0 : t * 128) + i * 32, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] *= f0;
+                    if constexpr (SPLIT) {
+                        if (n > 1) {
+                            float x[32];
+                            tmem_ld32(tO + 128 + i * 32, x);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                *reinterpret_cast<float4*>(other + r * D + (((i * 8 + k) ^ (r & 7)) * 4)) =
-                                    make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            for (int k = 0; k < 32; ++k) o[k] = fmaf(x[k], f1, o[k]);
                         }
                     }
-                }
-                named_bar_sync(1, 256);
-                if (t == 0) {
-                    const float m1 = ml[0][r], l1 = ml[1][r];
-                    const float mm = fmaxf(m, m1);
-                    const float zz = mm == -INFINITY ? 0.0f : mm;
-                    f0 = ex2(m - zz);
-                    f1 = n > 1 ? ex2(m1 - zz) : 0.0f;
-                    l = l * f0 + (n > 1 ? l1 * f1 : 0.0f);
-                    m = mm;
-                }
-            }
-            if ((!SPLIT || t == 0) && !aborted) {
-                const bool none = m == -INFINITY && l == 0.0f;
-                const float inv = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
-                float* part = p.part + (size_t)slot * slot_words(R, D);
-#pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
-                    float o[32];
-                    tmem_ld32(tO + i * 32, o);
-                    tmem_ld_wait();
-                    if constexpr (SPLIT) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= f0;
-                        if (n > 1) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float4 x = *reinterpret_cast<const float4*>(
-                                    other + r * D + (((i * 8 + k) ^ (r & 7)) * 4));
-                                o[4 * k] += x.x * f1; o[4 * k + 1] += x.y * f1;
-                                o[4 * k + 2] += x.z * f1; o[4 * k + 3] += x.w * f1;
-                            }
-                        }
-                    }
-                    if (live && whole) {
+                    if (out_live && out_whole) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint4 y;
-                            y.x = bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv);
-                            y.y = bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-                            y.z = bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-                            y.w = bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
-                            *reinterpret_cast<uint4*>(p.o + head * D + i * 32 + k * 8) = y;
+                            y.x = bf16x2(o[8 * k], o[8 * k + 1]);
+                            y.y = bf16x2(o[8 * k + 2], o[8 * k + 3]);
+                            y.z = bf16x2(o[8 * k + 4], o[8 * k + 5]);
+                            y.w = bf16x2(o[8 * k + 6], o[8 * k + 7]);
+                            *reinterpret_cast<uint4*>(p.o + out_head * D + i * 32 + k * 8) = y;
                         }
-                    } else if (live) {
+                    } else if (out_live) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             *reinterpret_cast<float4*>(part + (size_t)rb * D + i * 32 + k * 4) =
@@ -721,17 +945,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
                     }
                     __syncwarp();
                 }
-                if (live) {
-                    if (!whole) {
+                if (out_live && (!SPLIT || t == 0)) {
+                    if (!out_whole) {
                         part[(size_t)R * D + rb] = m;
                         part[(size_t)R * D + R + rb] = l;
                     } else if (p.lse) {
-                        p.lse[head] = none ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+                        p.lse[out_head] = none ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
                     }
                 }
             }
             tc_fence_before();
-            if constexpr (SPLIT) named_bar_sync(1, 256);       // the query rows' memory is free again
+            if constexpr (SPLIT) named_bar_sync(1, 256);   // all sums are read, Q is free
         }
     }
 
@@ -744,27 +968,30 @@ __global__ void __launch_bounds__(THREADS, 1) attend_umma_kernel(const AttendPar
 }
 
 template <int D, bool FP8, bool SELECTED, bool SPLIT>
-cudaError_t launch_one(const AttendParams& p, cudaStream_t st) {
+cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p, cudaStream_t st) {
     auto fn = attend_umma_kernel<D, FP8, SELECTED, SPLIT>;
-    constexpr int smem = UmmaShape<D, FP8>::SMEM;
-    static_assert(smem <= 227 * 1024 - 1024, "shared memory of a CTA (1 KB of it static)");
+    constexpr int smem = UmmaShape<D, FP8, SELECTED, SPLIT>::SMEM;
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    fn<<<p.ncta, THREADS, smem, st>>>(p);
+    fn<<<p.ncta, THREADS, smem, st>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
 template <int D, bool FP8>
-cudaError_t launch_type(const AttendParams& p, cudaStream_t st) {
-    if (p.idx) return launch_one<D, FP8, true, true>(p, st);
-    return p.R == 128 ? launch_one<D, FP8, false, true>(p, st) : launch_one<D, FP8, false, false>(p, st);
+cudaError_t launch_type(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p, cudaStream_t st) {
+    if (p.idx) return launch_one<D, FP8, true, true>(tk, tv, p, st);
+    return p.R == 128 ? launch_one<D, FP8, false, true>(tk, tv, p, st)
+                      : launch_one<D, FP8, false, false>(tk, tv, p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_umma(const AttendParams& p, cudaStream_t st) {
-    if (p.c.D == 128) return p.c.ks ? launch_type<128, true>(p, st) : launch_type<128, false>(p, st);
-    return p.c.ks ? launch_type<64, true>(p, st) : launch_type<64, false>(p, st);
+cudaError_t launch_attend_umma(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p,
+                               cudaStream_t st) {
+    if (p.c.D == 128)
+        return p.c.ks ? launch_type<128, true>(tk, tv, p, st) : launch_type<128, false>(tk, tv, p, st);
+    return p.c.ks ? launch_type<64, true>(tk, tv, p, st) : launch_type<64, false>(tk, tv, p, st);
 }
 
 }  // namespace pivot

@@ -104,6 +104,22 @@ pivot_status_t check_attend(const pivot_cache_t* cache, const pivot_attend_t* a,
     return PIVOT_OK;
 }
 
+// The plane as rows of tokens: a box is a page (at most 128 tokens) high, and
+// 64 bf16 values or one head's e4m3 codes wide.
+bool plane_map(CUtensorMap* map, const CacheView& c, void* plane) {
+    const TensorMapEncodeFn fn = tensor_map_encode();
+    if (!fn) return false;
+    const bool fp8 = c.ks != nullptr;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.Hkv * c.D, (cuuint64_t)c.num_pages * c.page_size()};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.rowb};
+    const cuuint32_t rows = c.page_size() < 128 ? c.page_size() : 128;
+    const cuuint32_t box[2] = {(cuuint32_t)(fp8 ? c.D : 64), rows}, steps[2] = {1, 1};
+    return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, plane, dims,
+              strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              fp8 && c.D == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t attend_layout(AttendParams* p, bool selected, void* ws) {
     size_t at = 0;
     uint8_t* base = static_cast<uint8_t*>(ws);
@@ -133,13 +149,15 @@ pivot_status_t attend(const pivot_cache_t* cache, const pivot_attend_t* a, bool 
     if (attend_layout(&p, selected, ws) > ws_bytes) return PIVOT_ERR_WORKSPACE;
     if (p.total == 0) return PIVOT_OK;
     cudaError_t e = cudaSuccess;
+    CUtensorMap tk, tv;
+    if (p.R > 32 && (!plane_map(&tk, p.c, p.c.k) || !plane_map(&tv, p.c, p.c.v))) return PIVOT_ERR_CUDA;
     if (!selected) {
         count_launch();
         e = launch_attend_plan(p, st);
         if (e != cudaSuccess) return status_of(e);
     }
     count_launch();
-    e = p.R > 32 ? launch_attend_umma(p, st) : launch_attend_rows(p, st);
+    e = p.R > 32 ? launch_attend_umma(tk, tv, p, st) : launch_attend_rows(p, st);
     if (e != cudaSuccess) return status_of(e);
     count_launch();
     return status_of(launch_attend_join(p, st));
