@@ -33,6 +33,12 @@ constexpr int TKEYS = 128;
 constexpr int THREADS = 384;
 constexpr int LOAD_WARP = 8, MMA_WARP = 11;
 
+// An mbarrier's count; a write to memory also for the compiler, which may move
+// it past the block's first barrier otherwise.
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -110,44 +116,36 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         : "r"(taddr));
 }
 
-// Weights 2^(c s + z) of 64 keys of a row: to TMEM in 16 bits (times the
-// values' scales for e4m3), and their sum.  The special-function unit gives
-// 16 exponentials a clock, which would take as long as the tile's products;
-// in a tile without masks POLY of every 16 are computed on the FMA pipe.
-constexpr int POLY = 4;
+// Weights 2^(c s + z) of 32 keys of a row: to TMEM in 16 bits (times the
+// values' scales for e4m3), and added to the sums.  The special-function unit
+// gives 16 exponentials a clock, which would take as long as the tile's
+// products; in a tile without masks POLY of every 16 are computed on the FMA
+// pipe.
+constexpr int POLY = 0;
 template <bool FP8, bool PLAIN>
-__device__ __forceinline__ float weights(float* s, float c, float z, const float* vs, uint32_t to) {
+__device__ __forceinline__ void weights(const float* s, float c, float z, const float* vs, uint32_t to,
+                                        uint64_t (&sum)[2]) {
     const uint64_t c2 = pack2(c, c), z2 = pack2(z, z);
-    uint64_t sum[2] = {0ull, 0ull};
+    uint32_t pk[16];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t pk[16];
+    for (int k = 0; k < 32; k += 4) {
+        float e[4];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            float* x = s + i * 32 + k;
-            float e[4];
-#pragma unroll
-            for (int y = 0; y < 4; y += 2) {
-                const uint64_t v = ffma2(pack2(x[y], x[y + 1]), c2, z2);
-                unpack2(v, e[y], e[y + 1]);
-                const bool poly = PLAIN && (k + y) % 16 < POLY;
-                e[y] = poly ? exp2_poly(e[y]) : ex2(e[y]);
-                e[y + 1] = poly ? exp2_poly(e[y + 1]) : ex2(e[y + 1]);
-                sum[y / 2] = add2(sum[y / 2], pack2(e[y], e[y + 1]));
-            }
-            if constexpr (FP8) {
-                const float4 v = *reinterpret_cast<const float4*>(vs + i * 32 + k);
-                e[0] *= v.x; e[1] *= v.y; e[2] *= v.z; e[3] *= v.w;
-            }
-            pk[k / 2] = FP8 ? f16x2(e[0], e[1]) : bf16x2(e[0], e[1]);
-            pk[k / 2 + 1] = FP8 ? f16x2(e[2], e[3]) : bf16x2(e[2], e[3]);
+        for (int y = 0; y < 4; y += 2) {
+            unpack2(ffma2(pack2(s[k + y], s[k + y + 1]), c2, z2), e[y], e[y + 1]);
+            const bool poly = PLAIN && (k + y) % 16 < POLY;
+            e[y] = poly ? exp2_poly(e[y]) : ex2(e[y]);
+            e[y + 1] = poly ? exp2_poly(e[y + 1]) : ex2(e[y + 1]);
+            sum[y / 2] = add2(sum[y / 2], pack2(e[y], e[y + 1]));
         }
-        tmem_st16(to + i * 16, pk);
+        if constexpr (FP8) {
+            const float4 v = *reinterpret_cast<const float4*>(vs + k);
+            e[0] *= v.x; e[1] *= v.y; e[2] *= v.z; e[3] *= v.w;
+        }
+        pk[k / 2] = FP8 ? f16x2(e[0], e[1]) : bf16x2(e[0], e[1]);
+        pk[k / 2 + 1] = FP8 ? f16x2(e[2], e[3]) : bf16x2(e[2], e[3]);
     }
-    float a, b, d, e;
-    unpack2(sum[0], a, b);
-    unpack2(sum[1], d, e);
-    return (a + b) + (d + e);
+    tmem_st16(to, pk);
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
@@ -224,30 +222,31 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&full[i], FP8 || SELECTED ? 2 : 1);
-            mbar_init(&empty[i], 1);
+            bar_init(&full[i], FP8 || SELECTED ? 2 : 1);
+            bar_init(&empty[i], 1);
         }
         for (int i = 0; i < S::CSTAGES; ++i) {
-            mbar_init(&cfull[i], 1);
-            mbar_init(&cempty[i], 2);
+            bar_init(&cfull[i], 1);
+            bar_init(&cempty[i], 2);
         }
         for (int i = 0; i < MS; ++i) {
-            mbar_init(&mfull[i], 1);
-            mbar_init(&mempty[i], SPLIT ? 4 : 8);
+            bar_init(&mfull[i], 1);
+            bar_init(&mempty[i], SPLIT ? 4 : 8);
         }
-        mbar_init(raw, 1);
+        bar_init(raw, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[2 * i], 4);
-            mbar_init(&pfull[2 * i + 1], 4);
-            mbar_init(&ofull[i], 1);
+            bar_init(&sfull[i], 1);
+            bar_init(&pfull[2 * i], 4);
+            bar_init(&pfull[2 * i + 1], 4);
+            bar_init(&ofull[i], 1);
         }
-        mbar_init(qfull, SPLIT ? 4 : 8);
-        mbar_init(drain, 1);
+        bar_init(qfull, SPLIT ? 4 : 8);
+        bar_init(drain, 1);
         fence_barrier_init();
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
     }
+    __syncwarp();
     if (warp == MMA_WARP) {
         tmem_alloc(tmem_at, 512);
         tmem_relinquish();
@@ -438,6 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t ms = 0, mph = 0;              // meta of the next tile to copy (or convert)
             uint32_t cs = 0, cph = 0;              // staging tile to convert
             uint32_t slot = 0, ph = 1;             // ring slot to fill
+            uint32_t out = 0;                      // and to publish
             const int es = FP8 ? 1 : 2;
             // e4m3: eight neighbouring lanes take four chunks of two keys
             // whose numbers differ in bits 0 and 2 (D = 64: in bit 0): their
@@ -491,35 +491,30 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (lane == 0) mbar_arrive(&full[at]);
                 };
                 if constexpr (!FP8) {
-                    // up to three tiles in flight; a slot is released once
-                    // the tile after its own is published at the latest, so
-                    // waiting for one with STAGES - 3 unpublished is safe
-                    constexpr int PENDING = STAGES >= 5 ? 2 : 1;
-                    uint32_t pend[PENDING];
-                    int npend = 0;
-                    for (int x = 0; x < total && !aborted; ++x) {
+                    // Tiles in flight.  The slot of a tile is released once
+                    // the tile after it is published at the latest, so the
+                    // slot waited for needs all but the STAGES - 2 tiles
+                    // before it published.
+                    constexpr int PENDING = STAGES - 3 < 3 ? STAGES - 3 : 3;
+                    auto publish_next = [&]() {
+                        publish(out);
+                        if (++out == STAGES) out = 0;
+                    };
+                    int x = 0;
+                    for (; x < total && !aborted; ++x) {
                         if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph))) aborted = true;
                         const uint32_t base = smem_u32(sT) + slot * S::TILE + (ch >> 3) * (TKEYS * 128);
                         if (!aborted && !copy(x, [&](int k) { return base + sw128_offset(k, ch & 7); }))
                             aborted = true;
                         cp_async_commit();
-                        if (npend == PENDING) {
-                            cp_async_wait<PENDING>();
-                            publish(pend[0]);
-#pragma unroll
-                            for (int i = 0; i + 1 < PENDING; ++i) pend[i] = pend[i + 1];
-                            --npend;
-                        }
-#pragma unroll
-                        for (int i = 0; i < PENDING; ++i)
-                            if (i == npend) pend[i] = slot;
-                        ++npend;
                         advance(slot, ph, STAGES);
+                        if (x >= PENDING) {
+                            cp_async_wait<PENDING>();
+                            publish_next();
+                        }
                     }
                     cp_async_wait<0>();
-#pragma unroll
-                    for (int i = 0; i < PENDING; ++i)
-                        if (i < npend) publish(pend[i]);
+                    for (int y = min(x, PENDING); y > 0; --y) publish_next();
                 } else {
                     // staging tiles are filled two ahead (selected: by these
                     // warps themselves, each its own keys)
@@ -699,7 +694,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         int ta, tz, slot;
         bool whole, live;
         size_t head;
-        uint4 qrow[D / 8];
         auto fetch = [&]() -> bool {
             while (u < u_end) {
                 it = find_item<SELECTED>(p, u);
@@ -712,11 +706,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 live = rb < it.rows;
                 const int rr = it.row0 + rb;
                 head = live ? (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G : 0;
-                if (NEEDS_Q1 || t == 0) {
-                    const uint4* src = reinterpret_cast<const uint4*>(p.q + head * D);
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) qrow[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                }
                 return true;
             }
             return false;
@@ -727,6 +716,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             // as halves, divided by the power of two under its largest value)
             float c = p.scale_log2;
             if (NEEDS_Q1 || t == 0) {
+                uint4 qrow[D / 8];
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + head * D);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) qrow[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
                 float down = 1.0f;
                 if constexpr (FP8) {
                     float amax = 0.0f;
@@ -779,47 +772,59 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sph ^= 1;
                 if (aborted) continue;
                 tc_fence_after();
-                float s[TKEYS];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, s + i * 32);
                 const uint4 okv = *reinterpret_cast<const uint4*>(m_ok + ms * 4);
-                tmem_ld_wait();
-                if constexpr (FP8) {
-                    const float4* ks = reinterpret_cast<const float4*>(m_ks + ms * TKEYS);
-#pragma unroll
-                    for (int i = 0; i < TKEYS / 4; ++i) {
-                        const float4 x = ks[i];
-                        s[4 * i] *= x.x; s[4 * i + 1] *= x.y; s[4 * i + 2] *= x.z; s[4 * i + 3] *= x.w;
-                    }
-                }
+                const float *ks = m_ks + ms * TKEYS, *vs = m_vs + ms * TKEYS;
                 const int key0 = (ta + j) * TKEYS;
                 const bool plain = (okv.x & okv.y & okv.z & okv.w) == 0xffffffffu &&
                                    (SELECTED || (key0 + TKEYS - 1 <= lim_lo &&
                                                  (!p.window || key0 > lim_hi - p.window)));
-                if (!plain) {
-                    const uint32_t ok[4] = {okv.x, okv.y, okv.z, okv.w};
-                    // keys from..to of the tile are this row's
-                    const int to = SELECTED ? TKEYS - 1 : min(lim - key0, TKEYS - 1);
-                    const int from = !SELECTED && p.window ? max(lim - p.window + 1 - key0, 0) : 0;
+                // keys from..to of the tile are this row's
+                const int to = SELECTED ? TKEYS - 1 : min(lim - key0, TKEYS - 1);
+                const int from = !SELECTED && p.window ? max(lim - p.window + 1 - key0, 0) : 0;
+                // scores of 32 keys, times the keys' scales, masked
+                auto finish = [&](float* s, int i) {
+                    if constexpr (FP8) {
+                        const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * i);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 x = k4[k];
+                            s[4 * k] *= x.x; s[4 * k + 1] *= x.y; s[4 * k + 2] *= x.z; s[4 * k + 3] *= x.w;
+                        }
+                    }
+                    if (!plain) {
+                        const uint32_t ok = i == 0 ? okv.x : i == 1 ? okv.y : i == 2 ? okv.z : okv.w;
                         const int a = min(max(from - 32 * i, 0), 32), z = min(max(to - 32 * i + 1, 0), 32);
                         const uint32_t below = z == 32 ? 0xffffffffu : (1u << z) - 1;
                         const uint32_t above = a == 32 ? 0u : 0xffffffffu << a;
-                        const uint32_t see = ok[i] & below & above;
+                        const uint32_t see = ok & below & above;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            s[32 * i + k] = (see >> k) & 1 ? s[32 * i + k] : -INFINITY;
+                        for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1 ? s[k] : -INFINITY;
                     }
-                }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                };
+                auto largest = [](const float* s, float (&mx)[4]) {
 #pragma unroll
-                for (int k = 4; k < TKEYS - 4; k += 8) {
+                    for (int k = 0; k < 32; k += 8)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[k + y], s[k + 4 + y]);
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[TKEYS - 4 + y]);
+                        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[k + y], s[k + 4 + y]);
+                };
+                // P takes the place of the first half of S, so the first half
+                // stays in registers and the second is read again for its
+                // exponentials: all 128 scores at once would not fit
+                float s0[64], s1[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tmem_ld32(tS + 64, s1);
+                tmem_ld32(tS + 96, s1 + 32);
+                tmem_ld_wait();
+                finish(s1, 2);
+                finish(s1 + 32, 3);
+                largest(s1, mx);
+                largest(s1 + 32, mx);
+                tmem_ld32(tS, s0);
+                tmem_ld32(tS + 32, s0 + 32);
+                tmem_ld_wait();
+                finish(s0, 0);
+                finish(s0 + 32, 1);
+                largest(s0, mx);
+                largest(s0 + 32, mx);
                 float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
                 if constexpr (FP8) top += m_lv[ms];
                 // The reference point m may lag behind the maximum by up to
@@ -849,17 +854,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 begun = true;
                 const float z = m == -INFINITY ? 0.0f : -m;
-                const float* vs = m_vs + ms * TKEYS;
+                uint64_t sum[2] = {0ull, 0ull};
+                auto weigh = [&](const float* s, int i) {
+                    if (plain) weights<FP8, true>(s, c, z, vs + 32 * i, tS + 16 * i, sum);
+                    else weights<FP8, false>(s, c, z, vs + 32 * i, tS + 16 * i, sum);
+                };
                 // the product with V starts on the first 64 keys' weights
                 // while the others' are computed
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    l += plain ? weights<FP8, true>(s + i * 64, c, z, vs + i * 64, tS + i * 32)
-                               : weights<FP8, false>(s + i * 64, c, z, vs + i * 64, tS + i * 32);
+                auto hand_over = [&](int half) {
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[2 * t + i]);
+                    if (lane == 0) mbar_arrive(&pfull[2 * t + half]);
+                };
+                weigh(s0, 0);
+                tmem_ld32(tS + 64, s1);
+                weigh(s0 + 32, 1);
+                hand_over(0);
+                tmem_ld_wait();
+                tmem_ld32(tS + 96, s1 + 32);
+                finish(s1, 2);
+                weigh(s1, 2);
+                tmem_ld_wait();
+                finish(s1 + 32, 3);
+                weigh(s1 + 32, 3);
+                hand_over(1);
+                {
+                    float a, b, d, e;
+                    unpack2(sum[0], a, b);
+                    unpack2(sum[1], d, e);
+                    l += (a + b) + (d + e);
                 }
                 if (lane == 0) mbar_arrive(&mempty[ms]);
             }
