@@ -344,3 +344,44 @@ def test_selected_attention(case, fp8):
     idx = idx.to(DEV)
     got = pv.selected_attention(c.c, q, offsets(counts), max(counts), idx, with_lse=True)
     agree(got, expected(c, q, counts, lens, idx=idx))
+
+
+# Runs of many key tiles a CTA: the ring, the split key tiles and the sums
+# that move, several items one after another.
+LONG = [
+    # counts, lengths, Hq, Hkv, D, page, window, topk
+    ([60], [5000], 64, 1, 128, 64, 0, 2048),
+    ([90, 40], [1500, 900], 40, 1, 64, 16, 0, 1500),
+    ([2] * 40, [30000] * 40, 40, 1, 128, 128, 0, 0),
+    ([20] * 12, [9000 + i for i in range(12)], 16, 4, 128, 32, 0, 0),
+    ([600], [20000], 32, 8, 64, 64, 3000, 0),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", LONG, ids=[str(i) for i in range(len(LONG))])
+def test_attention_over_many_tiles(case, fp8):
+    counts, lens, Hq, Hkv, D, page, window, topk = case
+    c, gen = fill(lens, page, Hkv, D, fp8, seed=Hq + topk)
+    total = sum(counts)
+    q = torch.randn(total, Hq, D, generator=gen).to(torch.bfloat16).to(DEV)
+    # scores that climb along the sequence: the reference point moves often
+    q *= torch.linspace(0.2, 6.0, total, device=DEV)[:, None, None].to(torch.bfloat16)
+    idx = None
+    if topk:
+        rows, at = [], 0
+        for b, n in enumerate(counts):
+            for i in range(n):
+                pos = lens[b] - n + i + 1
+                pick = torch.randperm(pos, generator=gen)[:topk].sort().values
+                rows.append(torch.nn.functional.pad(pick, (0, topk - len(pick)), value=-1))
+        idx = torch.stack(rows).to(torch.int32).to(DEV)
+        got = pv.selected_attention(c.c, q, offsets(counts), max(counts), idx, with_lse=True)
+    else:
+        got = pv.paged_attention(c.c, q, offsets(counts), max(counts), window=window, with_lse=True)
+    (o, lse), (ow, lw, size) = got, expected(c, q, counts, lens, window, idx)
+    torch.cuda.synchronize()
+    assert pv.device_error() == 0
+    # queries up to six times as long: six times the score error of O_TOL and LSE_TOL
+    assert bool(((o.double() - ow).abs() <= (2 * 2.0 ** -8 + 6 * 2.0 ** -10) * size + 1e-30).all())
+    assert float((lse.double() - lw).abs().max()) <= 6 * LSE_TOL

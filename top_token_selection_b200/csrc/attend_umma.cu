@@ -19,10 +19,16 @@
 // with cp.async (tile::gather4 was measured: about 75 cycles for four 128-byte
 // rows, a quarter of what the products take).
 //
-// Warps 0-3 and 4-7: softmax of tiles 0 and 1.  Warp 8: rows and TMA loads.
-// Warps 9 and 10: copies of selected keys, e4m3 codes to halves.  Warp 11:
-// MMA issue.  Three warps on each of the SM's four register files leave 168
-// registers a thread: the softmax holds its row's 128 scores.
+// Warps 0-15: softmax, four warps a tile and half of its keys.  Warp 16: rows
+// and TMA loads.  Warps 17 and 18: copies of selected keys, e4m3 codes to
+// halves.  Warp 19: MMA issue.
+//
+// What bounds it: the products.  On one SM a 128 x 128 x 16 product takes 96
+// cycles with both operands in shared memory and 75 with P in TMEM (64 would
+// be the nominal rate; measured back to back), 103 when the two alternate:
+// about 3300 cycles for 256 rows x 128 keys at D = 128.  The kernel takes
+// about 4250: a tile's softmax waits for its S, which waits for its last
+// product with V, and only two tiles fit into TMEM to fill the gap.
 #include "attend.h"
 
 namespace pivot {
@@ -30,8 +36,8 @@ namespace pivot {
 namespace {
 
 constexpr int TKEYS = 128;
-constexpr int THREADS = 384;
-constexpr int LOAD_WARP = 8, MMA_WARP = 11;
+constexpr int SOFT_WARPS = 16, LOAD_WARP = 16, MMA_WARP = 19;
+constexpr int THREADS = 640;
 
 // An mbarrier's count; a write to memory also for the compiler, which may move
 // it past the block's first barrier otherwise.
@@ -73,19 +79,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// 2^x of a number of at most 2^7 on the FMA pipe: x = n + f with n whole and
-// |f| <= 1/2 (the sum with 3 2^22 rounds to whole numbers), then a polynomial
-// of degree 4 for 2^f with value 1 at 0, fitted for the least relative error
-// (2.8e-6), and n added to the exponent.  Below -126 the result is 2^-126.
-__device__ __forceinline__ float exp2_poly(float x) {
-    x = fmaxf(x, -126.0f);
-    const float t = x + 12582912.0f;
-    const float f = x - (t - 12582912.0f);
-    float y = fmaf(f, 0.009582852944731712f, 0.055906426161527634f);
-    y = fmaf(y, f, 0.24024099111557007f);
-    y = fmaf(y, f, 0.6931241750717163f);
-    y = fmaf(y, f, 1.0f);
-    return __uint_as_float(__float_as_uint(y) + (__float_as_uint(t) << 23));
+// Whether `v` holds for any thread of a pair of warps (named barrier `id`).
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 // 16 32-bit columns of this thread's TMEM lane.
@@ -117,12 +120,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
 }
 
 // Weights 2^(c s + z) of 32 keys of a row: to TMEM in 16 bits (times the
-// values' scales for e4m3), and added to the sums.  The special-function unit
-// gives 16 exponentials a clock, which would take as long as the tile's
-// products; in a tile without masks POLY of every 16 are computed on the FMA
-// pipe.
-constexpr int POLY = 0;
-template <bool FP8, bool PLAIN>
+// values' scales for e4m3), and added to the sums.
+template <bool FP8>
 __device__ __forceinline__ void weights(const float* s, float c, float z, const float* vs, uint32_t to,
                                         uint64_t (&sum)[2]) {
     const uint64_t c2 = pack2(c, c), z2 = pack2(z, z);
@@ -133,9 +132,8 @@ __device__ __forceinline__ void weights(const float* s, float c, float z, const 
 #pragma unroll
         for (int y = 0; y < 4; y += 2) {
             unpack2(ffma2(pack2(s[k + y], s[k + y + 1]), c2, z2), e[y], e[y + 1]);
-            const bool poly = PLAIN && (k + y) % 16 < POLY;
-            e[y] = poly ? exp2_poly(e[y]) : ex2(e[y]);
-            e[y + 1] = poly ? exp2_poly(e[y + 1]) : ex2(e[y + 1]);
+            e[y] = ex2(e[y]);
+            e[y + 1] = ex2(e[y + 1]);
             sum[y / 2] = add2(sum[y / 2], pack2(e[y], e[y + 1]));
         }
         if constexpr (FP8) {
@@ -182,7 +180,7 @@ struct UmmaShape {
     // per tile: which keys count, and for e4m3 their scales; selected: rows
     static constexpr int MS = 8;
     static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 8 : 0) + (SELECTED ? TKEYS * 4 : 0));
-    static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 512;
+    static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 1024 + 512;
 };
 
 template <int D, bool FP8, bool SELECTED, bool SPLIT>
@@ -192,6 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     using S = UmmaShape<D, FP8, SELECTED, SPLIT>;
     constexpr int STAGES = S::STAGES, MS = S::MS;
     constexpr int R = SPLIT ? 128 : 256;
+    constexpr float LAG = FP8 ? 14.0f : 64.0f;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -204,7 +203,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     float* m_ks = m_lv + MS * 4;                          // [MS][128]
     float* m_vs = m_ks + MS * TKEYS;
     int* m_row = reinterpret_cast<int*>(FP8 ? m_vs + MS * TKEYS : m_lv);   // [MS][128] token rows
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sM + S::META);
+    uint32_t* m_top = reinterpret_cast<uint32_t*>(sM + S::META);   // [2][128] rows' maxima, as ordered_key
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sM + S::META + 1024);
     uint64_t* full = bars;                                // [STAGES] tile there
     uint64_t* empty = full + STAGES;                      // [STAGES] tile read
     uint64_t* mfull = empty + STAGES;                     // [MS] meta there
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < MS; ++i) {
             bar_init(&mfull[i], 1);
-            bar_init(&mempty[i], SPLIT ? 4 : 8);
+            bar_init(&mempty[i], SPLIT ? 8 : 16);
         }
         bar_init(raw, 1);
         for (int i = 0; i < 2; ++i) {
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bar_init(&pfull[2 * i + 1], 4);
             bar_init(&ofull[i], 1);
         }
-        bar_init(qfull, SPLIT ? 4 : 8);
+        bar_init(qfull, SPLIT ? 8 : 16);
         bar_init(drain, 1);
         fence_barrier_init();
         tma_prefetch_desc(&tmap_k);
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (leader) {
 #pragma unroll
                         for (int i = 4 * half; i < 4 * half + 4; ++i)
-                            umma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, b + i * (2048 >> 4),
+                            umma_ts(tmem + 256 + t * 128, tmem + t * 128 + half * 64 + (i & 3) * 8, b + i * (2048 >> 4),
                                     id_o, i > 0 ? 1u : (uint32_t)(h > 1));
                     }
                     __syncwarp();
@@ -677,55 +677,47 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else {
         // --------------------------------------------------------- softmax
-        const int t = warp >> 2;
+        // Stream t = tile of rows (or parity of the key tiles); two warps a
+        // TMEM lane quarter, x = 0, 1: keys 64 x .. of every tile, of the
+        // same rows.  Both weigh from one reference point m.
+        const int t = (warp >> 2) & 1, x = warp >> 3;
         const int r = (warp & 3) * 32 + lane;              // row of the tile, TMEM lane
         const int rb = SPLIT ? r : t * 128 + r;            // row of the block
+        const int pair = 1 + t * 4 + (warp & 3);           // named barrier of the two warps
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + 256;
-        constexpr bool NEEDS_Q1 = !SPLIT || FP8;           // the odd tiles' threads need their row
         uint32_t sph = 0, oph[2] = {0, 0};
         int tile_no = 0;
         bool aborted = false;
+        for (long long u = u_begin; u < u_end;) {
+            const Item it = find_item<SELECTED>(p, u);
+            const int ta = it.tile0 + (int)(u - it.unit0);
+            const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
+            const bool whole = it.unit0 >= u_begin && it.unit0 + it.tiles <= u_end;
+            const int slot = 2 * blockIdx.x + (it.unit0 < u_begin ? 0 : 1);
+            u = it.unit0 + (tz - it.tile0);
+            if (!it.ok) continue;
+            const int n = tz - ta;
+            const bool live = rb < it.rows;
+            const int rr = it.row0 + rb;
+            const size_t head = live ? (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G : 0;
+            const int lim = live ? it.pos0 + rr / p.G : -1;
+            const int lim_lo = it.pos0 + it.row0 / p.G;
+            const int lim_hi = it.pos0 + (it.row0 + it.rows - 1) / p.G;
 
-        // the run's items in turn; the next one and its query row are read
-        // while the last product of the one before is under way
-        long long u = u_begin;
-        Item it;
-        int ta, tz, slot;
-        bool whole, live;
-        size_t head;
-        auto fetch = [&]() -> bool {
-            while (u < u_end) {
-                it = find_item<SELECTED>(p, u);
-                ta = it.tile0 + (int)(u - it.unit0);
-                tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
-                whole = it.unit0 >= u_begin && it.unit0 + it.tiles <= u_end;
-                slot = 2 * blockIdx.x + (it.unit0 < u_begin ? 0 : 1);
-                u = it.unit0 + (tz - it.tile0);
-                if (!it.ok) continue;
-                live = rb < it.rows;
-                const int rr = it.row0 + rb;
-                head = live ? (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G : 0;
-                return true;
-            }
-            return false;
-        };
-        bool more = fetch();
-        while (more) {
-            // ---- this thread's query row into the swizzled tile (for e4m3
-            // as halves, divided by the power of two under its largest value)
+            // ---- this thread's half of its query row into the swizzled tile
+            // (for e4m3 as halves, divided by the power of two under the
+            // row's largest value)
             float c = p.scale_log2;
-            if (NEEDS_Q1 || t == 0) {
-                uint4 qrow[D / 8];
+            {
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + head * D);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) qrow[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
                 float down = 1.0f;
                 if constexpr (FP8) {
                     float amax = 0.0f;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
-                        const uint32_t w[4] = {qrow[i].x, qrow[i].y, qrow[i].z, qrow[i].w};
+                        const uint4 q = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
@@ -740,13 +732,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!SPLIT || t == 0) {
                     const uint32_t dst = smem_u32(sQ) + (SPLIT ? 0 : t * S::TILE);
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        uint32_t w[4] = {qrow[i].x, qrow[i].y, qrow[i].z, qrow[i].w};
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int i = x * (D / 16) + k;
+                        const uint4 q = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                        uint32_t w[4] = {q.x, q.y, q.z, q.w};
                         if constexpr (FP8) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = f16x2(__uint_as_float(w[k] << 16) * down,
-                                             __uint_as_float(w[k] & 0xFFFF0000u) * down);
+                            for (int y = 0; y < 4; ++y)
+                                w[y] = f16x2(__uint_as_float(w[y] << 16) * down,
+                                             __uint_as_float(w[y] & 0xFFFF0000u) * down);
                         }
                         sts16(dst + (i >> 3) * (TKEYS * 128) + sw128_offset(r, i & 7), w[0], w[1], w[2], w[3]);
                     }
@@ -755,48 +749,41 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (lane == 0) mbar_arrive(qfull);
                 }
             }
-            const int n = tz - ta;
-            const int lim = live ? it.pos0 + (it.row0 + rb) / p.G : -1;
-            const int lim_lo = it.pos0 + it.row0 / p.G;
-            const int lim_hi = it.pos0 + (it.row0 + it.rows - 1) / p.G;
 
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f;                 // l: of this thread's keys
+            if (x == 0) m_top[t * 128 + r] = 0;            // below every number; read after a barrier
             bool begun = false;                            // O holds sums
             for (int j = SPLIT ? t : 0; j < n; j += SPLIT ? 2 : 1) {
                 const int ms = (tile_no + j) % MS;
-                const uint32_t mph = (uint32_t)(((tile_no + j) / MS) & 1);
                 if (!aborted) {
+                    const uint32_t mph = (uint32_t)(((tile_no + j) / MS) & 1);
                     const bool got = mbar_wait(&sfull[t], sph) && mbar_wait(&mfull[ms], mph);
                     if (!__all_sync(0xffffffffu, got)) aborted = true;
                 }
                 sph ^= 1;
-                if (aborted) continue;
-                tc_fence_after();
-                const uint4 okv = *reinterpret_cast<const uint4*>(m_ok + ms * 4);
-                const float *ks = m_ks + ms * TKEYS, *vs = m_vs + ms * TKEYS;
-                const int key0 = (ta + j) * TKEYS;
-                const bool plain = (okv.x & okv.y & okv.z & okv.w) == 0xffffffffu &&
-                                   (SELECTED || (key0 + TKEYS - 1 <= lim_lo &&
-                                                 (!p.window || key0 > lim_hi - p.window)));
-                // keys from..to of the tile are this row's
-                const int to = SELECTED ? TKEYS - 1 : min(lim - key0, TKEYS - 1);
-                const int from = !SELECTED && p.window ? max(lim - p.window + 1 - key0, 0) : 0;
-                // scores of 32 keys, times the keys' scales, masked
+                const float *ks = m_ks + ms * TKEYS + 64 * x, *vs = m_vs + ms * TKEYS + 64 * x;
+                const uint2 ok = *reinterpret_cast<const uint2*>(m_ok + ms * 4 + 2 * x);
+                const int key0 = (ta + j) * TKEYS + 64 * x;
+                const bool plain = (ok.x & ok.y) == 0xffffffffu &&
+                                   (SELECTED || (key0 + 63 <= lim_lo && (!p.window || key0 > lim_hi - p.window)));
+                // scores of 32 of the 64 keys, times the keys' scales, masked
                 auto finish = [&](float* s, int i) {
                     if constexpr (FP8) {
                         const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * i);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float4 x = k4[k];
-                            s[4 * k] *= x.x; s[4 * k + 1] *= x.y; s[4 * k + 2] *= x.z; s[4 * k + 3] *= x.w;
+                            const float4 y = k4[k];
+                            s[4 * k] *= y.x; s[4 * k + 1] *= y.y; s[4 * k + 2] *= y.z; s[4 * k + 3] *= y.w;
                         }
                     }
                     if (!plain) {
-                        const uint32_t ok = i == 0 ? okv.x : i == 1 ? okv.y : i == 2 ? okv.z : okv.w;
+                        // keys from..to of these 64 are this row's
+                        const int to = SELECTED ? 63 : lim - key0;
+                        const int from = !SELECTED && p.window ? lim - p.window + 1 - key0 : 0;
                         const int a = min(max(from - 32 * i, 0), 32), z = min(max(to - 32 * i + 1, 0), 32);
                         const uint32_t below = z == 32 ? 0xffffffffu : (1u << z) - 1;
                         const uint32_t above = a == 32 ? 0u : 0xffffffffu << a;
-                        const uint32_t see = ok & below & above;
+                        const uint32_t see = (i ? ok.y : ok.x) & below & above;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1 ? s[k] : -INFINITY;
                     }
@@ -807,93 +794,89 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[k + y], s[k + 4 + y]);
                 };
-                // P takes the place of the first half of S, so the first half
-                // stays in registers and the second is read again for its
-                // exponentials: all 128 scores at once would not fit
-                float s0[64], s1[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                tmem_ld32(tS + 64, s1);
-                tmem_ld32(tS + 96, s1 + 32);
-                tmem_ld_wait();
-                finish(s1, 2);
-                finish(s1 + 32, 3);
-                largest(s1, mx);
-                largest(s1 + 32, mx);
-                tmem_ld32(tS, s0);
-                tmem_ld32(tS + 32, s0 + 32);
-                tmem_ld_wait();
-                finish(s0, 0);
-                finish(s0 + 32, 1);
-                largest(s0, mx);
-                largest(s0 + 32, mx);
-                float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-                if constexpr (FP8) top += m_lv[ms];
-                // The reference point m may lag behind the maximum by up to
-                // 8: weights then reach 2^8, which costs no precision, and
-                // the sums in TMEM seldom have to be multiplied.  For e4m3
-                // it stands over the weights times the values' scales, so
-                // that their product fits f16 whatever the scales; the sums
-                // of both are in its units, which cancel in o.
-                float f = 1.0f;
-                if (top > m + 8.0f) {
-                    f = m == -INFINITY ? 0.0f : ex2(m - top);
-                    m = top;
+                // The reference point may lag behind the maximum by LAG:
+                // weights then reach 2^LAG, which costs no precision (bf16 has
+                // the exponents of fp32; f16 ends at 2^16), and m and the sums
+                // in TMEM seldom have to move (with a lag of 8 a move, which
+                // takes about 900 cycles, came in every other tile of rows
+                // with a few heavy keys).  For e4m3 m stands over the weights
+                // times the values' scales, so that their product fits f16
+                // whatever the scales; the sums of both are in its units,
+                // which cancel in o.
+                float top = -INFINITY;
+                if (!aborted) {
+                    float a[32], b[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tc_fence_after();
+                    tmem_ld32(tS + 64 * x, a);
+                    tmem_ld32(tS + 64 * x + 32, b);
+                    tmem_ld_wait();
+                    finish(a, 0);
+                    finish(b, 1);
+                    largest(a, mx);
+                    largest(b, mx);
+                    top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+                    if constexpr (FP8) top += m_lv[ms];
                 }
-                l *= f;
-                if (__any_sync(0xffffffffu, f != 1.0f) && begun) {
-                    // the product that wrote O was complete before this S was
-#pragma unroll 1
-                    for (int i = 0; i < D / 16; ++i) {
-                        uint32_t o[16];
-                        tmem_ld16(tO + t * 128 + i * 16, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st16(tO + t * 128 + i * 16, o);
+                if (pair_any(pair, top > m + LAG)) {
+                    atomicMax(&m_top[t * 128 + r], ordered_key(top));
+                    named_bar_sync(pair, 64);
+                    top = key_to_float(m_top[t * 128 + r]);
+                    float f = 1.0f;
+                    if (top > m + LAG) {
+                        f = m == -INFINITY ? 0.0f : ex2(m - top);
+                        m = top;
                     }
-                    tmem_st_wait();
+                    l *= f;
+                    // the product that wrote O was complete before this S was;
+                    // each warp takes half of the values
+                    if (begun && !aborted) {
+#pragma unroll 1
+                        for (int i = x * (D / 32); i < (x + 1) * (D / 32); ++i) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + t * 128 + i * 16, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(tO + t * 128 + i * 16, o);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
+                    named_bar_sync(pair, 64);      // all of the row's sums have moved
                 }
-                begun = true;
+                if (aborted) continue;
                 const float z = m == -INFINITY ? 0.0f : -m;
-                uint64_t sum[2] = {0ull, 0ull};
-                auto weigh = [&](const float* s, int i) {
-                    if (plain) weights<FP8, true>(s, c, z, vs + 32 * i, tS + 16 * i, sum);
-                    else weights<FP8, false>(s, c, z, vs + 32 * i, tS + 16 * i, sum);
-                };
-                // the product with V starts on the first 64 keys' weights
-                // while the others' are computed
-                auto hand_over = [&](int half) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[2 * t + half]);
-                };
-                weigh(s0, 0);
-                tmem_ld32(tS + 64, s1);
-                weigh(s0 + 32, 1);
-                hand_over(0);
-                tmem_ld_wait();
-                tmem_ld32(tS + 96, s1 + 32);
-                finish(s1, 2);
-                weigh(s1, 2);
-                tmem_ld_wait();
-                finish(s1 + 32, 3);
-                weigh(s1 + 32, 3);
-                hand_over(1);
+                begun = true;
+                // P takes the place of these 64 keys' S, half of it at a time:
+                // the scores are read again, for all 64 would not fit in the
+                // registers beside the rest
                 {
-                    float a, b, d, e;
-                    unpack2(sum[0], a, b);
-                    unpack2(sum[1], d, e);
-                    l += (a + b) + (d + e);
+                    uint64_t sum[2] = {0ull, 0ull};
+                    float a[32];
+                    tmem_ld32(tS + 64 * x, a);
+                    tmem_ld_wait();
+                    finish(a, 0);
+                    weights<FP8>(a, c, z, vs, tS + 64 * x, sum);
+                    tmem_ld32(tS + 64 * x + 32, a);
+                    tmem_ld_wait();
+                    finish(a, 1);
+                    weights<FP8>(a, c, z, vs + 32, tS + 64 * x + 16, sum);
+                    float s0, s1, s2, s3;
+                    unpack2(sum[0], s0, s1);
+                    unpack2(sum[1], s2, s3);
+                    l += (s0 + s1) + (s2 + s3);
                 }
-                if (lane == 0) mbar_arrive(&mempty[ms]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&pfull[2 * t + x]);
+                    mbar_arrive(&mempty[ms]);
+                }
             }
             tile_no += n;
 
             // ---- the item's end
-            const bool out_whole = whole, out_live = live;
-            const size_t out_head = head;
-            float* part = p.part + (size_t)slot * slot_words(R, D);
-            more = fetch();
             if (!aborted) {
                 bool got = true;
 #pragma unroll
@@ -905,81 +888,97 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (!__all_sync(0xffffffffu, got)) aborted = true;
             }
-            tc_fence_after();
-            float f0 = 1.0f, f1 = 0.0f;                    // of tile 0's and 1's sums
-            if constexpr (SPLIT) {
-                // both halves' threads of a row join the sums of the even and
-                // odd tiles, half of the values each (TMEM lanes belong to
-                // warps by their number modulo 4, so both can read both)
-                // columns of S that P leaves free carry the statistics over
-                tmem_st2(tS + 64, __float_as_uint(m), __float_as_uint(l));
-                tmem_st_wait();
-                tc_fence_before();
-                named_bar_sync(1, 256);
-                tc_fence_after();
-                uint32_t om, ol;
-                tmem_ld2(tmem + lane_off + (t ^ 1) * 128 + 64, om, ol);
-                tmem_ld_wait();
-                const float mt[2] = {t ? __uint_as_float(om) : m, t ? m : __uint_as_float(om)};
-                const float lt[2] = {t ? __uint_as_float(ol) : l, t ? l : __uint_as_float(ol)};
-                m = fmaxf(mt[0], mt[1]);                   // tile 1 without keys: -inf, 0
-                const float zz = m == -INFINITY ? 0.0f : m;
-                f0 = ex2(mt[0] - zz);
-                f1 = ex2(mt[1] - zz);
-                l = lt[0] * f0 + lt[1] * f1;
-            }
+            // Columns of S that P leaves free carry the statistics from warp
+            // to warp (TMEM lanes belong to warps by their number modulo 4).
+            // Split key tiles: four warps a row join the two streams' sums, a
+            // quarter of the values each.
             if (!aborted) {
+                tc_fence_after();
+                tmem_st2(tS + 32 + 2 * x, __float_as_uint(m), __float_as_uint(l));
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            if constexpr (SPLIT) named_bar_sync(9, SOFT_WARPS * 32);
+            else named_bar_sync(pair, 64);
+            tc_fence_after();
+            if (!aborted) {
+                float f0 = 1.0f, f1 = 0.0f;                // of the streams' sums
+                if constexpr (SPLIT) {
+                    uint32_t sm[2], sl[2], y;
+                    float ls[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_ld2(tmem + lane_off + k * 128 + 32, sm[k], sl[0]);
+                        tmem_ld2(tmem + lane_off + k * 128 + 34, y, sl[1]);
+                        tmem_ld_wait();
+                        ls[k] = __uint_as_float(sl[0]) + __uint_as_float(sl[1]);
+                    }
+                    const float m0 = __uint_as_float(sm[0]), m1 = __uint_as_float(sm[1]);
+                    m = fmaxf(m0, m1);                     // a stream without keys: -inf, 0
+                    const float zz = m == -INFINITY ? 0.0f : m;
+                    f0 = ex2(m0 - zz);
+                    f1 = ex2(m1 - zz);
+                    l = ls[0] * f0 + ls[1] * f1;
+                } else {
+                    uint32_t om, ol;
+                    tmem_ld2(tS + 32 + 2 * (x ^ 1), om, ol);
+                    tmem_ld_wait();
+                    l += __uint_as_float(ol);
+                }
                 const bool none = m == -INFINITY && l == 0.0f;
-                const float inv = out_whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
-                constexpr int PARTS = SPLIT ? D / 64 : D / 32;     // 32 values each
-                const int first = SPLIT ? t * PARTS : 0;
+                const float inv = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
+                constexpr int PARTS = SPLIT ? D / 64 : D / 32;     // 16 values each
+                const int first = (SPLIT ? 2 * t + x : x) * PARTS;
+                float* part = p.part + (size_t)slot * slot_words(R, D);
                 f0 *= inv;
                 f1 *= inv;
-#pragma unroll 1
+#pragma unroll
                 for (int i = first; i < first + PARTS; ++i) {
-                    float o[32];
-                    tmem_ld32(tO + (SPLIT ? 0 : t * 128) + i * 32, o);
+                    float o[16];
+                    tmem_ld16(tO + (SPLIT ? 0 : t * 128) + i * 16, reinterpret_cast<uint32_t*>(o));
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] *= f0;
+                    for (int k = 0; k < 16; ++k) o[k] *= f0;
                     if constexpr (SPLIT) {
                         if (n > 1) {
-                            float x[32];
-                            tmem_ld32(tO + 128 + i * 32, x);
+                            float o1[16];
+                            tmem_ld16(tO + 128 + i * 16, reinterpret_cast<uint32_t*>(o1));
                             tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = fmaf(x[k], f1, o[k]);
+                            for (int k = 0; k < 16; ++k) o[k] = fmaf(o1[k], f1, o[k]);
                         }
                     }
-                    if (out_live && out_whole) {
+                    if (live && whole) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 2; ++k) {
                             uint4 y;
                             y.x = bf16x2(o[8 * k], o[8 * k + 1]);
                             y.y = bf16x2(o[8 * k + 2], o[8 * k + 3]);
                             y.z = bf16x2(o[8 * k + 4], o[8 * k + 5]);
                             y.w = bf16x2(o[8 * k + 6], o[8 * k + 7]);
-                            *reinterpret_cast<uint4*>(p.o + out_head * D + i * 32 + k * 8) = y;
+                            *reinterpret_cast<uint4*>(p.o + head * D + i * 16 + k * 8) = y;
                         }
-                    } else if (out_live) {
+                    } else if (live) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<float4*>(part + (size_t)rb * D + i * 32 + k * 4) =
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<float4*>(part + (size_t)rb * D + i * 16 + k * 4) =
                                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                     __syncwarp();
                 }
-                if (out_live && (!SPLIT || t == 0)) {
-                    if (!out_whole) {
+                if (live && x == 0 && (!SPLIT || t == 0)) {
+                    if (!whole) {
                         part[(size_t)R * D + rb] = m;
                         part[(size_t)R * D + R + rb] = l;
                     } else if (p.lse) {
-                        p.lse[out_head] = none ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+                        p.lse[head] = none ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
                     }
                 }
             }
             tc_fence_before();
-            if constexpr (SPLIT) named_bar_sync(1, 256);   // all sums are read, Q is free
+            // all statistics are read (and, split, all sums and Q)
+            if constexpr (SPLIT) named_bar_sync(9, SOFT_WARPS * 32);
+            else named_bar_sync(pair, 64);
         }
     }
 
