@@ -6,9 +6,9 @@
 // 128 query rows on the M axis (the 128 TMEM lanes), so one thread owns one
 // row's softmax and no shuffle is needed; 128 keys a tile.  P goes back to
 // TMEM in 16 bits, over the S it came from, and is the A operand of the second
-// product (bf16 beside bf16 values; e4m3 codes are converted to f16, which
-// holds them exactly, and P is f16 then).  Two such tiles are in flight and take turns: while one's softmax
-// runs, the tensor cores work on the other.  They are
+// product: bf16 beside bf16 values, f16 beside e4m3 ones, which are converted
+// to f16 with their scales.  Two such tiles are in flight and take turns:
+// while one's softmax runs, the tensor cores work on the other.  They are
 //  * the two halves of a block of 256 rows, which share every key tile; or
 //  * (SPLIT) the even and odd key tiles of one block of up to 128 rows, each
 //    with sums of its own that are joined at the end.
@@ -20,8 +20,8 @@
 // rows, a quarter of what the products take).
 //
 // Warps 0-15: softmax, four warps a tile and half of its keys.  Warp 16: rows
-// and TMA loads.  Warps 17 and 18: copies of selected keys, e4m3 codes to
-// halves.  Warp 19: MMA issue.
+// and TMA loads.  Warp 17: MMA issue.  Warps 18-21 (selected keys, e4m3
+// codes): copies, and codes to halves.
 //
 // What bounds it: the products.  On one SM a 128 x 128 x 16 product takes 96
 // cycles with both operands in shared memory and 75 with P in TMEM (64 would
@@ -36,8 +36,8 @@ namespace pivot {
 namespace {
 
 constexpr int TKEYS = 128;
-constexpr int SOFT_WARPS = 16, LOAD_WARP = 16, MMA_WARP = 19;
-constexpr int THREADS = 640;
+constexpr int SOFT_WARPS = 16, LOAD_WARP = 16, MMA_WARP = 17;
+constexpr int COPY_WARP = 18, COPY_WARPS = 4;      // e4m3 or selected only
 
 // An mbarrier's count; a write to memory also for the compiler, which may move
 // it past the block's first barrier otherwise.
@@ -73,6 +73,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -89,6 +94,19 @@ __device__ __forceinline__ bool pair_any(int id, bool v) {
         : "r"((uint32_t)v), "r"(id)
         : "memory");
     return r != 0;
+}
+
+// 2^e of a whole number within [-100, 100].
+__device__ __forceinline__ float exp2_whole(float e) { return __uint_as_float((uint32_t)(127 + (int)e) << 23); }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// A number rounded to 7 significant bits.
+__device__ __forceinline__ float seven_bits(float a) {
+    const uint32_t u = __float_as_uint(a);
+    return __uint_as_float((u + 0xFFFFu + ((u >> 17) & 1u)) & 0xFFFE0000u);
 }
 
 // 16 32-bit columns of this thread's TMEM lane.
@@ -119,26 +137,28 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         : "r"(taddr));
 }
 
-// Weights 2^(c s + z) of 32 keys of a row: to TMEM in 16 bits (times the
-// values' scales for e4m3), and added to the sums.
+// Weights 2^(c s + z) of 32 keys of a row (e4m3: 2^(c s rest + z)): to TMEM in
+// 16 bits, and added to the sums.
 template <bool FP8>
-__device__ __forceinline__ void weights(const float* s, float c, float z, const float* vs, uint32_t to,
+__device__ __forceinline__ void weights(const float* s, float c, float z, const float* rest, uint32_t to,
                                         uint64_t (&sum)[2]) {
     const uint64_t c2 = pack2(c, c), z2 = pack2(z, z);
     uint32_t pk[16];
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
         float e[4];
+        uint64_t cr[2] = {c2, c2};
+        if constexpr (FP8) {
+            const float4 r = *reinterpret_cast<const float4*>(rest + k);
+            cr[0] = mul2(c2, pack2(r.x, r.y));
+            cr[1] = mul2(c2, pack2(r.z, r.w));
+        }
 #pragma unroll
         for (int y = 0; y < 4; y += 2) {
-            unpack2(ffma2(pack2(s[k + y], s[k + y + 1]), c2, z2), e[y], e[y + 1]);
+            unpack2(ffma2(pack2(s[k + y], s[k + y + 1]), cr[y / 2], z2), e[y], e[y + 1]);
             e[y] = ex2(e[y]);
             e[y + 1] = ex2(e[y + 1]);
             sum[y / 2] = add2(sum[y / 2], pack2(e[y], e[y + 1]));
-        }
-        if constexpr (FP8) {
-            const float4 v = *reinterpret_cast<const float4*>(vs + k);
-            e[0] *= v.x; e[1] *= v.y; e[2] *= v.z; e[3] *= v.w;
         }
         pk[k / 2] = FP8 ? f16x2(e[0], e[1]) : bf16x2(e[0], e[1]);
         pk[k / 2 + 1] = FP8 ? f16x2(e[2], e[3]) : bf16x2(e[2], e[3]);
@@ -173,18 +193,23 @@ struct UmmaShape {
     static constexpr int QTILES = SPLIT ? 1 : 2;
     // ring slots: as many as fit beside Q (and the staging tiles)
     static constexpr int STAGES = D == 64 ? 8 : (FP8 ? 3 : 5) + (SPLIT && (FP8 || !SELECTED) ? 1 : 0);
+    static constexpr int WARPS = FP8 || SELECTED ? COPY_WARP + COPY_WARPS : COPY_WARP;
+    static constexpr int THREADS = WARPS * 32;
+    // registers are per SM sub-partition (16K each; warp w runs on w % 4)
+    static constexpr int REGS = WARPS > 20 ? 80 : 96;
+    static_assert((WARPS + 3) / 4 * 32 * REGS <= 16384, "register file of a sub-partition");
     // bf16 is loaded into the ring; e4m3 codes into staging tiles, from which
     // they are converted into the ring
     static constexpr int CSTAGES = 3;
     static constexpr int STAGING = FP8 ? CSTAGES * TKEYS * D : 0;
     // per tile: which keys count, and for e4m3 their scales; selected: rows
     static constexpr int MS = 8;
-    static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 8 : 0) + (SELECTED ? TKEYS * 4 : 0));
+    static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 12 : 0) + (SELECTED ? TKEYS * 4 : 0));
     static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 1024 + 512;
 };
 
 template <int D, bool FP8, bool SELECTED, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     attend_umma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const AttendParams p) {
     using S = UmmaShape<D, FP8, SELECTED, SPLIT>;
@@ -199,9 +224,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* sC = sT + STAGES * S::TILE;                  // e4m3 codes on their way
     uint8_t* sM = sC + S::STAGING;
     uint32_t* m_ok = reinterpret_cast<uint32_t*>(sM);     // [MS][4]
-    float* m_lv = reinterpret_cast<float*>(sM + MS * 16); // [MS] see log2_above
-    float* m_ks = m_lv + MS * 4;                          // [MS][128]
-    float* m_vs = m_ks + MS * TKEYS;
+    float* m_lv = reinterpret_cast<float*>(sM + MS * 16); // [MS] log2_above of the scales of V
+    float* m_lk = m_lv + MS;                              // [MS] and of K
+    float* m_ks = m_lv + MS * 4;                          // [MS][128] scales over those
+    float* m_rest = m_ks + MS * TKEYS;                    // [MS][128] what m_ks leaves of a key's scale
+    float* m_vs = m_rest + MS * TKEYS;
     int* m_row = reinterpret_cast<int*>(FP8 ? m_vs + MS * TKEYS : m_lv);   // [MS][128] token rows
     uint32_t* m_top = reinterpret_cast<uint32_t*>(sM + S::META);   // [2][128] rows' maxima, as ordered_key
     uint64_t* bars = reinterpret_cast<uint64_t*>(sM + S::META + 1024);
@@ -222,16 +249,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            bar_init(&full[i], FP8 || SELECTED ? 2 : 1);
+            bar_init(&full[i], FP8 || SELECTED ? COPY_WARPS : 1);
             bar_init(&empty[i], 1);
         }
         for (int i = 0; i < S::CSTAGES; ++i) {
             bar_init(&cfull[i], 1);
-            bar_init(&cempty[i], 2);
+            bar_init(&cempty[i], COPY_WARPS);
         }
         for (int i = 0; i < MS; ++i) {
             bar_init(&mfull[i], 1);
-            bar_init(&mempty[i], SPLIT ? 8 : 16);
+            bar_init(&mempty[i], (SPLIT ? 8 : 16) + (FP8 ? COPY_WARPS : 0));
         }
         bar_init(raw, 1);
         for (int i = 0; i < 2; ++i) {
@@ -350,13 +377,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                         make_int4(row[0] >= 0 ? row[0] : spare, row[1] >= 0 ? row[1] : spare,
                                   row[2] >= 0 ? row[2] : spare, row[3] >= 0 ? row[3] : spare);
                 if constexpr (FP8) {
+                    // scales relative to the power of two at or above the
+                    // tile's largest
+                    const float lk = log2_above(fmaxf(fmaxf(fabsf(ks[0]), fabsf(ks[1])),
+                                                      fmaxf(fabsf(ks[2]), fabsf(ks[3]))));
                     const float lv = log2_above(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
                                                       fmaxf(fabsf(vs[2]), fabsf(vs[3]))));
-                    if (lane == 0) m_lv[ms] = lv;
-                    *reinterpret_cast<float4*>(m_ks + ms * TKEYS + 4 * lane) =
-                        make_float4(ks[0], ks[1], ks[2], ks[3]);
+                    const float dk = exp2_whole(-lk), dv = exp2_whole(-lv);
+                    if (lane == 0) {
+                        m_lk[ms] = lk;
+                        m_lv[ms] = lv;
+                    }
+                    // a key's scale in two factors: 7 bits that go into its
+                    // halves, exactly (a code has 4), and the rest, within
+                    // 2^-7 of 1, for the fp32 scores
+                    float h[4], rest[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = ks[i] * dk;
+                        h[i] = seven_bits(a);
+                        rest[i] = h[i] == 0.0f ? 1.0f : __fdividef(a, h[i]);
+                    }
+                    *reinterpret_cast<float4*>(m_ks + ms * TKEYS + 4 * lane) = make_float4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<float4*>(m_rest + ms * TKEYS + 4 * lane) =
+                        make_float4(rest[0], rest[1], rest[2], rest[3]);
                     *reinterpret_cast<float4*>(m_vs + ms * TKEYS + 4 * lane) =
-                        make_float4(vs[0], vs[1], vs[2], vs[3]);
+                        make_float4(vs[0] * dv, vs[1] * dv, vs[2] * dv, vs[3] * dv);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&mfull[ms]);
@@ -427,15 +473,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t e = loaded - 1 - i;
             mbar_wait(&there[e % RING], (e / RING) & 1);
         }
-    } else if (warp > LOAD_WARP && warp < MMA_WARP) {
+    } else if (warp >= COPY_WARP) {
         // ------------------- selected keys; e4m3 codes to halves (exact)
-        // Two warps, 64 keys of each tile each.  Selected keys are copied
+        // Four warps, 32 keys of each tile each.  Selected keys are copied
         // row by row: bf16 into the ring, codes into the staging tiles.
         if constexpr (FP8 || SELECTED) {
-            const int w64 = (warp - LOAD_WARP - 1) * 64;
+            constexpr int KEYS = TKEYS / COPY_WARPS;           // of a warp
+            const int key_w = (warp - COPY_WARP) * KEYS;
             bool aborted = false;
             uint32_t ms = 0, mph = 0;              // meta of the next tile to copy (or convert)
-            uint32_t cs = 0, cph = 0;              // staging tile to convert
+            uint32_t cs = 0, cph = 0, cms = 0;     // staging tile to convert, and its meta
             uint32_t slot = 0, ph = 1;             // ring slot to fill
             uint32_t out = 0;                      // and to publish
             const int es = FP8 ? 1 : 2;
@@ -448,11 +495,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             auto key_of = [&](int j) -> int {                  // of instruction j
                 if constexpr (FP8 && D == 128) {
                     const int q = (lane >> 2) & 3;
-                    return w64 + (j >> 1) * 8 + (((j & 1) * 2 + (q >> 1)) ^ ((q & 1) * 5));
+                    return key_w + (j >> 1) * 8 + (((j & 1) * 2 + (q >> 1)) ^ ((q & 1) * 5));
                 } else if constexpr (FP8) {
-                    return w64 + j * 8 + (lane >> 2);
+                    return key_w + j * 8 + (lane >> 2);
                 } else {
-                    return w64 + j * KPI + lane / CH;
+                    return key_w + j * KPI + lane / CH;
                 }
             };
             auto code_at = [&](uint32_t stage, int k) -> uint32_t {
@@ -478,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if ((x & 1) == 0 && !__all_sync(0xffffffffu, mbar_wait(&mfull[ms], mph))) return false;
                     const uint8_t* plane = ((x & 1) ? p.c.v : p.c.k) + head_off;
 #pragma unroll
-                    for (int j = 0; j < 64 / KPI; ++j) {
+                    for (int j = 0; j < KEYS / KPI; ++j) {
                         const int k = key_of(j);
                         cp_async16(dst(k), plane + (size_t)m_row[ms * TKEYS + k] * p.c.rowb);
                     }
@@ -538,19 +585,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                             aborted = true;
                             break;
                         }
-                        uint32_t ok[2] = {0xffffffffu, 0xffffffffu};
+                        uint32_t ok = 0xffffffffu;
                         if constexpr (!SELECTED) {             // values that do not count: 0
-                            if (x & 1) {
-                                ok[0] = m_ok[ms * 4 + (w64 >> 5)];
-                                ok[1] = m_ok[ms * 4 + (w64 >> 5) + 1];
-                                advance(ms, mph, MS);
-                            }
+                            if (x & 1) ok = m_ok[cms * 4 + (key_w >> 5)];
                         }
-                        const bool every = (ok[0] & ok[1]) == 0xffffffffu;
+                        const bool every = ok == 0xffffffffu;
                         const uint32_t dst = smem_u32(sT) + slot * S::TILE + (ch >> 2) * (TKEYS * 128);
-                        constexpr int BATCH = 8;               // reads before the writes
+                        constexpr int BATCH = KEYS / KPI;      // reads before the writes
 #pragma unroll
-                        for (int j0 = 0; j0 < 64 / KPI; j0 += BATCH) {
+                        for (int j0 = 0; j0 < KEYS / KPI; j0 += BATCH) {
                             uint4 c[BATCH];
 #pragma unroll
                             for (int j = 0; j < BATCH; ++j)
@@ -561,23 +604,30 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (!every) {
 #pragma unroll
                                 for (int j = 0; j < BATCH; ++j) {
-                                    const int k = key_of(j0 + j) - w64;
-                                    if (!((ok[k >> 5] >> (k & 31)) & 1)) c[j] = make_uint4(0, 0, 0, 0);
+                                    if (!((ok >> (key_of(j0 + j) - key_w)) & 1)) c[j] = make_uint4(0, 0, 0, 0);
                                 }
                             }
 #pragma unroll
                             for (int j = 0; j < BATCH; ++j) {
                                 const uint32_t v[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+                                const int k = key_of(j0 + j), c0 = 2 * (ch & 3);
                                 uint32_t y[8];
+                                // times the key's 7 bits: exact; times the
+                                // value's 11: two errors of up to 2^-12
+                                const float m = ((x & 1) ? m_vs : m_ks)[cms * TKEYS + k];
+                                const uint32_t m2 = f16x2(m, m);
 #pragma unroll
                                 for (int n = 0; n < 4; ++n) {
-                                    y[2 * n] = e4m3x2_f16x2((uint16_t)(v[n] & 0xFFFFu));
-                                    y[2 * n + 1] = e4m3x2_f16x2((uint16_t)(v[n] >> 16));
+                                    y[2 * n] = mul_f16x2(e4m3x2_f16x2((uint16_t)(v[n] & 0xFFFFu)), m2);
+                                    y[2 * n + 1] = mul_f16x2(e4m3x2_f16x2((uint16_t)(v[n] >> 16)), m2);
                                 }
-                                const int k = key_of(j0 + j), c0 = 2 * (ch & 3);
                                 sts16(dst + sw128_offset(k, c0), y[0], y[1], y[2], y[3]);
                                 sts16(dst + sw128_offset(k, c0 + 1), y[4], y[5], y[6], y[7]);
                             }
+                        }
+                        if (x & 1) {                           // the tile's scales are read
+                            if (lane == 0) mbar_arrive(&mempty[cms]);
+                            if (++cms == MS) cms = 0;
                         }
                         publish(slot);
                         if (!SELECTED && lane == 0) mbar_arrive(&cempty[cs]);
@@ -761,21 +811,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!__all_sync(0xffffffffu, got)) aborted = true;
                 }
                 sph ^= 1;
-                const float *ks = m_ks + ms * TKEYS + 64 * x, *vs = m_vs + ms * TKEYS + 64 * x;
+                // e4m3: factor of the tile's scores, and log2 of its values'
+                const float ct = FP8 ? c * exp2_whole(m_lk[ms]) : c, lv = FP8 ? m_lv[ms] : 0.0f;
                 const uint2 ok = *reinterpret_cast<const uint2*>(m_ok + ms * 4 + 2 * x);
                 const int key0 = (ta + j) * TKEYS + 64 * x;
                 const bool plain = (ok.x & ok.y) == 0xffffffffu &&
                                    (SELECTED || (key0 + 63 <= lim_lo && (!p.window || key0 > lim_hi - p.window)));
-                // scores of 32 of the 64 keys, times the keys' scales, masked
+                // the scores of keys that do not count
                 auto finish = [&](float* s, int i) {
-                    if constexpr (FP8) {
-                        const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * i);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 y = k4[k];
-                            s[4 * k] *= y.x; s[4 * k + 1] *= y.y; s[4 * k + 2] *= y.z; s[4 * k + 3] *= y.w;
-                        }
-                    }
                     if (!plain) {
                         // keys from..to of these 64 are this row's
                         const int to = SELECTED ? 63 : lim - key0;
@@ -805,17 +848,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // which cancel in o.
                 float top = -INFINITY;
                 if (!aborted) {
-                    float a[32], b[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float a[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     tc_fence_after();
-                    tmem_ld32(tS + 64 * x, a);
-                    tmem_ld32(tS + 64 * x + 32, b);
-                    tmem_ld_wait();
-                    finish(a, 0);
-                    finish(b, 1);
-                    largest(a, mx);
-                    largest(b, mx);
-                    top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-                    if constexpr (FP8) top += m_lv[ms];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        tmem_ld32(tS + 64 * x + 32 * i, a);
+                        tmem_ld_wait();
+                        finish(a, i);
+                        largest(a, mx);
+                    }
+                    top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * ct + lv;
+                    // e4m3: without the rest of the scales, up to 2^-7 off
+                    if (FP8 && top > -INFINITY) top += fabsf(top - lv) * 0.0078125f;
                 }
                 if (pair_any(pair, top > m + LAG)) {
                     atomicMax(&m_top[t * 128 + r], ordered_key(top));
@@ -845,7 +889,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     named_bar_sync(pair, 64);      // all of the row's sums have moved
                 }
                 if (aborted) continue;
-                const float z = m == -INFINITY ? 0.0f : -m;
+                const float z = m == -INFINITY ? 0.0f : lv - m;
                 begun = true;
                 // P takes the place of these 64 keys' S, half of it at a time:
                 // the scores are read again, for all 64 would not fit in the
@@ -856,15 +900,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld32(tS + 64 * x, a);
                     tmem_ld_wait();
                     finish(a, 0);
-                    weights<FP8>(a, c, z, vs, tS + 64 * x, sum);
+                    weights<FP8>(a, ct, z, m_rest + ms * TKEYS + 64 * x, tS + 64 * x, sum);
                     tmem_ld32(tS + 64 * x + 32, a);
                     tmem_ld_wait();
                     finish(a, 1);
-                    weights<FP8>(a, c, z, vs + 32, tS + 64 * x + 16, sum);
+                    weights<FP8>(a, ct, z, m_rest + ms * TKEYS + 64 * x + 32, tS + 64 * x + 16, sum);
                     float s0, s1, s2, s3;
                     unpack2(sum[0], s0, s1);
                     unpack2(sum[1], s2, s3);
-                    l += (s0 + s1) + (s2 + s3);
+                    l += ((s0 + s1) + (s2 + s3)) * (FP8 ? exp2_whole(-lv) : 1.0f);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -997,7 +1041,7 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Atten
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    fn<<<p.ncta, THREADS, smem, st>>>(tk, tv, p);
+    fn<<<p.ncta, UmmaShape<D, FP8, SELECTED, SPLIT>::THREADS, smem, st>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
