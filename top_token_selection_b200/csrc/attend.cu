@@ -21,6 +21,7 @@ constexpr int PLAN_THREADS = 1024;
 __global__ void __launch_bounds__(PLAN_THREADS) attend_plan_kernel(const AttendParams p) {
     __shared__ int tmp[33];
     const int B = p.c.B;
+    let_next_start();
     // row blocks before each sequence
     int carry = 0;
     for (int b0 = 0; b0 < B; b0 += PLAN_THREADS) {
@@ -185,10 +186,15 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c4 = lane & 3;
+    let_next_start();
+    if constexpr (!SELECTED) wait_for_previous();
     const long long units = total_units<SELECTED>(p);
-    const long long u_end = run_begin(units, blockIdx.x + 1, p.ncta);
-    long long u = run_begin(units, blockIdx.x, p.ncta);
+    const int ncta = run_count(p, units);
+    const bool used = (int)blockIdx.x < ncta;
+    const long long u_end = used ? run_begin(units, blockIdx.x + 1, ncta) : 0;
+    long long u = used ? run_begin(units, blockIdx.x, ncta) : 0;
     const long long u_begin = u;
+    if (u == u_end && threadIdx.x == 0) p.join[blockIdx.x].rows = 0;
     const uint32_t my_ring = smem_u32(ring) + warp * (S::STAGES * S::STAGE);
     float* my_scales = scales + warp * (S::STAGES * 2 * KW);
 
@@ -198,6 +204,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
         const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
         const bool whole = it.unit0 >= u_begin && it.unit0 + it.tiles <= u_end;
         const int slot = 2 * blockIdx.x + (it.unit0 < u_begin ? 0 : 1);
+        if (u == u_begin && threadIdx.x == 0) put_join(p, it, units, u_begin, blockIdx.x, ncta);
         u = it.unit0 + (tz - it.tile0);
         if (!it.ok) continue;
 
@@ -637,67 +644,63 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
 }
 
 // ---------------------------------------------------------------- the join
-// Block (c, y): if the first unit of CTA c's run lies inside an item that
-// no earlier run boundary lies in, a warp joins each of its rows.
-template <int D, bool SELECTED>
+// A warp a row of the item whose record CTA blockIdx.x + 1 of the call left.
+template <int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) {
-    const int c = blockIdx.x + 1;
-    const long long units = total_units<SELECTED>(p);
-    if (units == 0) return;
-    const long long u = run_begin(units, c, p.ncta);
-    if (u >= units || u == run_begin(units, c - 1, p.ncta)) return;
-    const Item it = find_item<SELECTED>(p, u);
-    if (!it.ok || it.unit0 == u) return;                        // the boundary splits nothing
-    const int c0 = run_of(units, it.unit0, p.ncta);
-    // the first boundary inside the item is the begin of the next run with work
-    if (run_begin(units, c0 + 1, p.ncta) != u) return;
-    const int c1 = run_of(units, it.unit0 + it.tiles - 1, p.ncta);
+    wait_for_previous();
+    const JoinRecord j = p.join[blockIdx.x + 1];
     const int lane = threadIdx.x & 31;
+    const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
+    if (r >= j.rows) return;
     constexpr int PER = D / 32;
-    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < it.rows; r += gridDim.y * 4) {
-        const size_t words = slot_words(p.R, D);
-        // maxima and sums: a lane a partial
-        float mx = -INFINITY;
-        for (int i = c0 + lane; i <= c1; i += 32) {
-            const float* s = p.part + (size_t)(2 * i + (i == c0)) * words + (size_t)p.R * D;
-            if (run_begin(units, i, p.ncta) < run_begin(units, i + 1, p.ncta)) mx = fmaxf(mx, s[r]);
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float z = mx == -INFINITY ? 0.0f : mx;
-        float sum = 0.0f, o[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) o[j] = 0.0f;
-        for (int i0 = c0; i0 <= c1; i0 += 32) {
-            const int i = i0 + lane;
-            float f = 0.0f;
-            if (i <= c1 && run_begin(units, i, p.ncta) < run_begin(units, i + 1, p.ncta)) {
-                const float* s = p.part + (size_t)(2 * i + (i == c0)) * words + (size_t)p.R * D;
-                f = ex2(s[r] - z);
-                sum += s[p.R + r] * f;
-            }
-            const int n = min(32, c1 - i0 + 1);
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, k);
-                if (fk == 0.0f) continue;                       // nothing there (or all of it masked)
-                const float* s = p.part + (size_t)(2 * (i0 + k) + (i0 + k == c0)) * words + (size_t)r * D;
-#pragma unroll
-                for (int j = 0; j < PER; ++j) o[j] += s[lane * PER + j] * fk;
-            }
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const int rr = it.row0 + r;
-        const size_t head = (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G;
-        const bool none = mx == -INFINITY && sum == 0.0f;
-        const float inv = none ? 0.0f : 1.0f / sum;
-        uint32_t* to = reinterpret_cast<uint32_t*>(p.o + head * D + lane * PER);
-#pragma unroll
-        for (int j = 0; j < PER; j += 2) to[j / 2] = bf16x2(o[j] * inv, o[j + 1] * inv);
-        if (p.lse && lane == 0)
-            p.lse[head] = none ? -INFINITY : (z + __log2f(sum)) * 0.6931471805599453f;
+    const size_t words = slot_words(p.R, D);
+    // a CTA without units left nothing
+    auto there = [&](int i) { return i <= j.c1 && run_begin(j.units, i, j.ncta) < run_begin(j.units, i + 1, j.ncta); };
+    auto sums = [&](int i) { return p.part + (size_t)(2 * i + (i == j.c0)) * words; };
+    // a lane a partial: its maximum and sum
+    float m = -INFINITY, l = 0.0f;
+    for (int i = j.c0 + lane; i <= j.c1; i += 32) {
+        if (!there(i)) continue;
+        const float* s = sums(i) + (size_t)p.R * D;
+        const float mi = s[r], li = s[p.R + r];
+        const float top = fmaxf(m, mi);
+        const float z = top == -INFINITY ? 0.0f : top;
+        l = l * ex2(m - z) + li * ex2(mi - z);
+        m = top;
     }
+    float mx = m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const float z = mx == -INFINITY ? 0.0f : mx;
+    float sum = l * ex2(m - z), o[PER];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) o[k] = 0.0f;
+    // four partials at a time: their loads do not wait for one another
+    for (int i0 = j.c0; i0 <= j.c1; i0 += 4) {
+        float x[4][PER], f[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const bool ok = there(i0 + y);
+            const float* s = sums(ok ? i0 + y : j.c0);
+            f[y] = ok ? ex2(s[(size_t)p.R * D + r] - z) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) x[y][k] = s[(size_t)r * D + lane * PER + k];
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int k = 0; k < PER; ++k) o[k] = f[y] == 0.0f ? o[k] : fmaf(x[y][k], f[y], o[k]);
+    }
+    const int rr = j.row0 + r;
+    const size_t head = (size_t)(j.first + rr / p.G) * p.Hq + j.h * p.G + rr % p.G;
+    const bool none = mx == -INFINITY && sum == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / sum;
+    uint32_t* to = reinterpret_cast<uint32_t*>(p.o + head * D + lane * PER);
+#pragma unroll
+    for (int k = 0; k < PER; k += 2) to[k / 2] = bf16x2(o[k] * inv, o[k + 1] * inv);
+    if (p.lse && lane == 0) p.lse[head] = none ? -INFINITY : (z + __log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, bool FP8, int MT, bool SELECTED>
@@ -707,8 +710,7 @@ cudaError_t launch_rows_one(const AttendParams& p, cudaStream_t st) {
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs an SM");
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    fn<<<p.ncta, 128, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch(!SELECTED, fn, p.ncta, 128, smem, st, p);
 }
 
 template <int D, bool FP8, bool SELECTED>
@@ -728,7 +730,9 @@ size_t attend_plan_bytes(int B, int total, int G, int R) {
     const size_t blocks = (size_t)((long long)total * G / R) + B;
     return (size_t)(B + 1) * 8 + blocks * 8 + (size_t)(B + 1) * 4;
 }
-size_t attend_part_bytes(int ncta, int R, int D) { return (size_t)ncta * 2 * R * (D + 2) * 4; }
+size_t attend_part_bytes(int ncta, int R, int D) {
+    return (size_t)ncta * (sizeof(JoinRecord) + (size_t)2 * R * (D + 2) * 4);
+}
 
 cudaError_t launch_attend_plan(const AttendParams& p, cudaStream_t st) {
     attend_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(p);
@@ -742,15 +746,9 @@ cudaError_t launch_attend_rows(const AttendParams& p, cudaStream_t st) {
 
 cudaError_t launch_attend_join(const AttendParams& p, cudaStream_t st) {
     if (p.ncta < 2) return cudaSuccess;
-    const dim3 grid(p.ncta - 1, p.R / 16 < 16 ? p.R / 4 : 16);
-    if (p.idx) {
-        if (p.c.D == 128) attend_join_kernel<128, true><<<grid, 128, 0, st>>>(p);
-        else attend_join_kernel<64, true><<<grid, 128, 0, st>>>(p);
-    } else {
-        if (p.c.D == 128) attend_join_kernel<128, false><<<grid, 128, 0, st>>>(p);
-        else attend_join_kernel<64, false><<<grid, 128, 0, st>>>(p);
-    }
-    return cudaGetLastError();
+    const dim3 grid(p.ncta - 1, p.R / 4);
+    return p.c.D == 128 ? launch(true, attend_join_kernel<128>, grid, 128, 0, st, p)
+                        : launch(true, attend_join_kernel<64>, grid, 128, 0, st, p);
 }
 
 }  // namespace pivot

@@ -1,6 +1,8 @@
 // attend.h -- attention over the paged cache: parameters and launchers.
 #pragma once
 
+#include <utility>
+
 #include "paged.cuh"
 
 namespace pivot {
@@ -31,8 +33,20 @@ struct AttendParams {
     // partial sums: slots 2c (a CTA's item that began before its run) and
     // 2c + 1 (one that it began): R rows of D sums, then R maxima, R sums
     float* part;
+    // per CTA: what to join where its run begins inside an item
+    struct JoinRecord* join;
     int ncta;
 };
+
+// Partial sums of one item: CTAs c0 .. c1 worked on it (c0 began it); rows = 0
+// where there is nothing to join.
+struct JoinRecord {
+    long long units;
+    int c0, c1, ncta;
+    int first, h, row0, rows;
+    int pad[3];
+};
+static_assert(sizeof(JoinRecord) == 48, "three 16-byte reads");
 
 // One item and where it lies among the units.
 struct Item {
@@ -63,6 +77,14 @@ __device__ __forceinline__ long long total_units(const AttendParams& p) {
     }
 }
 
+// CTAs that share the units.  On the rows kernel, whose units are small, a call
+// of few units keeps to few CTAs, three units each, so that an item leaves few
+// partial sums to join.
+__device__ __forceinline__ int run_count(const AttendParams& p, long long units) {
+    const int ncta = p.ncta;
+    const long long n = p.R > 32 ? units : units / 3;
+    return n < 1 ? 1 : n < ncta ? (int)n : ncta;
+}
 // First unit of CTA c's run.
 __device__ __forceinline__ long long run_begin(long long units, int c, int ncta) {
     return units * c / ncta;
@@ -146,6 +168,48 @@ __device__ __forceinline__ float log2_above(float scale) {
     if (top == 0) return 0.0f;
     const int e = (int)((top + 0x007FFFFFu) >> 23) - 127;
     return (float)(e < -100 ? -100 : e > 100 ? 100 : e);
+}
+
+// One thread of each CTA: the record of the item that holds the first unit of
+// its run, if an earlier CTA began it and no other CTA's run begins between.
+__device__ __forceinline__ void put_join(const AttendParams& p, const Item& it, long long units, long long u_begin,
+                                         int c, int ncta) {
+    JoinRecord r{};
+    if (it.ok && it.unit0 < u_begin) {
+        r.c0 = run_of(units, it.unit0, ncta);
+        if (run_begin(units, r.c0 + 1, ncta) == u_begin) {
+            r.units = units;
+            r.c1 = run_of(units, it.unit0 + it.tiles - 1, ncta);
+            r.ncta = ncta;
+            r.first = it.first;
+            r.h = it.h;
+            r.row0 = it.row0;
+            r.rows = it.rows;
+        }
+    }
+    p.join[c] = r;
+}
+
+// Programmatic dependent launch: a kernel lets the next one of its call be
+// set up beside it, and waits for the one before to be complete.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// after: the kernel waits for the one before itself (wait_for_previous).
+template <class... Formal, class... Actual>
+inline cudaError_t launch(bool after, void (*fn)(Formal...), dim3 grid, dim3 block, int smem, cudaStream_t st,
+                          Actual&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, std::forward<Actual>(args)...);
 }
 
 __device__ __forceinline__ size_t slot_words(int R, int D) { return (size_t)R * (D + 2); }

@@ -283,9 +283,13 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
 
+    let_next_start();
+    if constexpr (!SELECTED) wait_for_previous();
     const long long units = total_units<SELECTED>(p);
-    const long long u_begin = run_begin(units, blockIdx.x, p.ncta);
-    const long long u_end = run_begin(units, blockIdx.x + 1, p.ncta);
+    const int ncta = run_count(p, units);
+    const bool used = (int)blockIdx.x < ncta;
+    const long long u_begin = used ? run_begin(units, blockIdx.x, ncta) : 0;
+    const long long u_end = used ? run_begin(units, blockIdx.x + 1, ncta) : 0;
 
     if (warp == LOAD_WARP) {
         // ------------------------------------------------------- rows, loads
@@ -302,10 +306,12 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
         constexpr uint32_t RING = FP8 ? S::CSTAGES : STAGES;
         const int box = min(TKEYS, p.c.page_size());           // keys of a TMA box
         const int boxes = TKEYS / box;
+        if (u_begin == u_end && lane == 0) p.join[blockIdx.x].rows = 0;
         for (long long u = u_begin; u < u_end && !aborted;) {
             const Item it = find_item<SELECTED>(p, u);
             const int ta = it.tile0 + (int)(u - it.unit0);
             const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
+            if (u == u_begin && lane == 0) put_join(p, it, units, u_begin, blockIdx.x, ncta);
             u = it.unit0 + (tz - it.tile0);
             if (!it.ok) continue;
             const int lim_lo = it.pos0 + it.row0 / p.G;
@@ -1041,8 +1047,7 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Atten
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    fn<<<p.ncta, UmmaShape<D, FP8, SELECTED, SPLIT>::THREADS, smem, st>>>(tk, tv, p);
-    return cudaGetLastError();
+    return launch(!SELECTED, fn, p.ncta, UmmaShape<D, FP8, SELECTED, SPLIT>::THREADS, smem, st, tk, tv, p);
 }
 
 template <int D, bool FP8>

@@ -130,7 +130,8 @@ size_t attend_layout(AttendParams* p, bool selected, void* ws) {
         p->blk_off = reinterpret_cast<int32_t*>(p->blk_units + blocks);
         at = up(attend_plan_bytes(p->c.B, p->total, p->G, p->R));
     }
-    p->part = reinterpret_cast<float*>(base + at);
+    p->join = reinterpret_cast<JoinRecord*>(base + at);
+    p->part = reinterpret_cast<float*>(p->join + p->ncta);
     return at + up(attend_part_bytes(p->ncta, p->R, p->c.D));
 }
 
