@@ -708,7 +708,8 @@ cudaError_t launch_rows_one(const AttendParams& p, cudaStream_t st) {
     auto fn = attend_rows_kernel<D, FP8, MT, SELECTED>;
     constexpr int smem = RowsShape<D, FP8, MT>::SMEM;
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs an SM");
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static bool done[64] = {false};
+    const cudaError_t e = allow_smem(fn, smem, done);
     if (e != cudaSuccess) return e;
     return launch(!SELECTED, fn, p.ncta, 128, smem, st, p);
 }

@@ -195,6 +195,17 @@ __device__ __forceinline__ void put_join(const AttendParams& p, const Item& it, 
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Dynamic shared memory of kernel `fn` on the current device, set once.
+template <class F>
+inline cudaError_t allow_smem(F* fn, int smem, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+}
+
 // after: the kernel waits for the one before itself (wait_for_previous).
 template <class... Formal, class... Actual>
 inline cudaError_t launch(bool after, void (*fn)(Formal...), dim3 grid, dim3 block, int smem, cudaStream_t st,

@@ -1045,7 +1045,8 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Atten
     auto fn = attend_umma_kernel<D, FP8, SELECTED, SPLIT>;
     constexpr int smem = UmmaShape<D, FP8, SELECTED, SPLIT>::SMEM;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static bool done[64] = {false};
+    const cudaError_t e = allow_smem(fn, smem, done);
     if (e != cudaSuccess) return e;
     return launch(!SELECTED, fn, p.ncta, UmmaShape<D, FP8, SELECTED, SPLIT>::THREADS, smem, st, tk, tv, p);
 }

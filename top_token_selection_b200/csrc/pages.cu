@@ -159,9 +159,20 @@ __global__ void __launch_bounds__(256)
                     *vs = reinterpret_cast<const uint4*>(c.v) + src * page16;
         uint4 *kd = reinterpret_cast<uint4*>(c.k) + dst * page16,
               *vd = reinterpret_cast<uint4*>(c.v) + dst * page16;
-        for (size_t i = threadIdx.x; i < n16; i += blockDim.x) {
-            kd[i] = ks[i];
-            vd[i] = vs[i];
+        for (size_t i0 = threadIdx.x; i0 < n16; i0 += 4 * 256) {
+            uint4 x[4], y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i0 + 256 * j < n16) {
+                    x[j] = ks[i0 + 256 * j];
+                    y[j] = vs[i0 + 256 * j];
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i0 + 256 * j < n16) {
+                    kd[i0 + 256 * j] = x[j];
+                    vd[i0 + 256 * j] = y[j];
+                }
         }
         if (c.ks)
             for (int i = threadIdx.x; i < rem; i += blockDim.x) {
@@ -185,7 +196,15 @@ __global__ void __launch_bounds__(256)
     const uint4* src = reinterpret_cast<const uint4*>(value ? v_new : k_new) + (size_t)r * n8;
     uint8_t* plane = (value ? c.v : c.k) + (size_t)row * c.rowb;
     if (!c.ks) {
-        for (int i = lane; i < n8; i += 32) reinterpret_cast<uint4*>(plane)[i] = src[i];
+        for (int i0 = lane; i0 < n8; i0 += 128) {
+            uint4 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i0 + 32 * j < n8) x[j] = __ldcs(src + i0 + 32 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i0 + 32 * j < n8) reinterpret_cast<uint4*>(plane)[i0 + 32 * j] = x[j];
+        }
         return;
     }
     float amax = 0.0f;
@@ -224,7 +243,7 @@ __device__ bool ids_ok(const int32_t* ids, int n, int B, bool distinct, uint32_t
 }
 
 // Pair by pair: the source's row is noted and its pages gain a reference...
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     fork_take_kernel(const CacheView c, const int32_t* src, const int32_t* dst, int n, int32_t* ws) {
     extern __shared__ uint32_t seen[];
     if (!ids_ok(dst, n, c.B, true, seen) || !ids_ok(src, n, c.B, false, seen)) {
@@ -247,7 +266,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // ...then every destination gives up its own pages and gets the noted row.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     fork_give_kernel(const CacheView c, const int32_t* src, const int32_t* dst, int n,
                      const int32_t* ws) {
     extern __shared__ uint32_t seen[];
@@ -263,7 +282,7 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x == 0) c.len[d] = ws[i];
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     free_kernel(const CacheView c, const int32_t* seqs, const int32_t* keep, int n) {
     extern __shared__ uint32_t seen[];
     bool ok = ids_ok(seqs, n, c.B, true, seen);
@@ -309,15 +328,17 @@ __global__ void __launch_bounds__(256)
                 const int32_t* src_ids, const int32_t* dst_ids, int n) {
     const int pieces = (int)((bytes + PIECE - 1) / PIECE);
     const long long jobs = (long long)n * pieces;
+    // the same piece of every page, then the next: copies of one source read
+    // it from L2 together (48 copies of 16 rows of 8 MB: 95 -> 83 us)
     for (long long j = blockIdx.x; j < jobs; j += gridDim.x) {
-        const int i = (int)(j / pieces);
+        const int i = (int)(j % n);
         const int a = src_ids[i], b = dst_ids[i];
         if ((unsigned)a >= (unsigned)src_pages || (unsigned)b >= (unsigned)dst_pages) {
             if (threadIdx.x == 0) raise_error(ERRBIT_DATA);
             continue;
         }
         copy_piece(src + (size_t)a * bytes, dst + (size_t)b * bytes, bytes,
-                   (size_t)(j % pieces) * PIECE);
+                   (size_t)(j / n) * PIECE);
     }
 }
 
@@ -335,22 +356,35 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     compact_plan_kernel(const CacheView c, int32_t* used_out, int32_t* ws) {
     __shared__ int tmp[33];
     const CompactWs w(ws, c.num_pages);
+    constexpr int PER = 8;                // pages a thread takes at a time
     int mine = 0;
     for (int p = threadIdx.x; p < c.num_pages; p += PLAN_THREADS) mine += c.refs[p] > 0;
     int used;
     block_exclusive(mine, tmp, used);
     int moves = 0, holes = 0;
-    for (int base = 0; base < c.num_pages; base += PLAN_THREADS) {
-        const int p = base + threadIdx.x;
-        const bool in = p < c.num_pages;
-        const bool live = in && c.refs[p] > 0;
-        const int of = live && p >= used, to = in && !live && p < used;
+    for (int base = 0; base < c.num_pages; base += PLAN_THREADS * PER) {
+        const int p0 = base + threadIdx.x * PER;
+        uint32_t live = 0, in = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (p0 + i < c.num_pages) {
+                in |= 1u << i;
+                live |= (uint32_t)(c.refs[p0 + i] > 0) << i;
+            }
+        uint32_t low = 0;                 // ids below U
+#pragma unroll
+        for (int i = 0; i < PER; ++i) low |= (uint32_t)(p0 + i < used) << i;
+        const uint32_t of = live & ~low, to = in & ~live & low;
         int tot;
-        // both ranks in one scan: at most 1024 of each
-        const int x = block_exclusive(of | (to << 16), tmp, tot);
-        if (of) w.of[moves + (x & 0xFFFF)] = p;
-        if (to) w.to[holes + (x >> 16)] = p;
-        if (in) w.remap[p] = live ? p : -1;
+        // both ranks in one scan: at most 8192 of each
+        const int x = block_exclusive(__popc(of) | (__popc(to) << 16), tmp, tot);
+        int a = moves + (x & 0xFFFF), b = holes + (x >> 16);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if ((of >> i) & 1) w.of[a++] = p0 + i;
+            if ((to >> i) & 1) w.to[b++] = p0 + i;
+            if ((in >> i) & 1) w.remap[p0 + i] = (live >> i) & 1 ? p0 + i : -1;
+        }
         moves += tot & 0xFFFF;
         holes += tot >> 16;
     }
@@ -404,6 +438,8 @@ __global__ void __launch_bounds__(256)
 }
 
 size_t seen_bytes(int B) { return (size_t)((B + 31) / 32) * 4; }
+// Threads of a block that walks one table row.
+int row_threads(int max_pages) { return max_pages > 512 ? 1024 : 256; }
 
 }  // namespace
 
@@ -426,14 +462,14 @@ cudaError_t launch_append(const CacheView& c, const void* k_new, const void* v_n
 
 cudaError_t launch_fork(const CacheView& c, const int32_t* src, const int32_t* dst, int n,
                         int32_t* ws, cudaStream_t st) {
-    fork_take_kernel<<<n, 256, seen_bytes(c.B), st>>>(c, src, dst, n, ws);
-    fork_give_kernel<<<n, 256, seen_bytes(c.B), st>>>(c, src, dst, n, ws);
+    fork_take_kernel<<<n, row_threads(c.max_pages), seen_bytes(c.B), st>>>(c, src, dst, n, ws);
+    fork_give_kernel<<<n, row_threads(c.max_pages), seen_bytes(c.B), st>>>(c, src, dst, n, ws);
     return cudaGetLastError();
 }
 
 cudaError_t launch_free(const CacheView& c, const int32_t* seqs, const int32_t* keep, int n,
                         cudaStream_t st) {
-    free_kernel<<<n, 256, seen_bytes(c.B), st>>>(c, seqs, keep, n);
+    free_kernel<<<n, row_threads(c.max_pages), seen_bytes(c.B), st>>>(c, seqs, keep, n);
     return cudaGetLastError();
 }
 

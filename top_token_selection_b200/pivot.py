@@ -560,8 +560,8 @@ class _On:
     below allocate belongs to the stream that uses it."""
 
     def __init__(self, t, stream):
-        self.ctx = []
-        if t.device.index != torch.cuda.current_device():
+        self.ctx, self.index = [], t.device.index
+        if self.index != torch.cuda.current_device():
             self.ctx.append(torch.cuda.device(t.device))
         if stream is not None:
             self.ctx.append(torch.cuda.stream(stream))
@@ -569,7 +569,7 @@ class _On:
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(torch.cuda.current_stream(self.index).cuda_stream)
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
@@ -577,14 +577,15 @@ class _On:
 
 
 def _arg(t, name, dtype, shape, device):
-    """`t` if it is a contiguous tensor of that type, shape (None: any) and device; raises if not."""
+    """The address of `t` if it is a contiguous tensor of that type, shape and
+    device; raises if not."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name}: a {dtype} tensor is wanted")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: wanted contiguous, on {device}")
-    return t
+    return t.data_ptr()
 
 
 def make_cache(k, v, table, length, refs, k_scale=None, v_scale=None) -> PivotCache:
@@ -598,17 +599,15 @@ def make_cache(k, v, table, length, refs, k_scale=None, v_scale=None) -> PivotCa
     B, columns = table.shape
     dev, i32 = k.device, torch.int32
     code = _dtype_code(k)
-    _arg(k, "k", k.dtype, k.shape, dev)
-    _arg(v, "v", k.dtype, k.shape, dev)
-    _arg(table, "table", i32, (B, columns), dev)
-    _arg(length, "length", i32, (B,), dev)
-    _arg(refs, "refs", i32, (n,), dev)
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None:
-            _arg(t, name, torch.float32, (n, page), dev)
-    c = PivotCache(code, B, Hkv, D, page, n, columns, _p(k), _p(v), _p(k_scale), _p(v_scale),
-                   _p(table), _p(length), _p(refs))
+    f32 = torch.float32
+    c = PivotCache(code, B, Hkv, D, page, n, columns, _arg(k, "k", k.dtype, k.shape, dev),
+                   _arg(v, "v", k.dtype, k.shape, dev),
+                   None if k_scale is None else _arg(k_scale, "k_scale", f32, (n, page), dev),
+                   None if v_scale is None else _arg(v_scale, "v_scale", f32, (n, page), dev),
+                   _arg(table, "table", i32, (B, columns), dev),
+                   _arg(length, "length", i32, (B,), dev), _arg(refs, "refs", i32, (n,), dev))
     c._keep = (k, v, k_scale, v_scale, table, length, refs)
+    c.device = dev
     return c
 
 
@@ -616,41 +615,40 @@ def cache_append(cache: PivotCache, k_new, v_new, cu_new, max_new, ws=None, stre
     """Append rows cu_new[b] .. cu_new[b + 1] of k_new, v_new (bf16
     [total, Hkv, D]) to sequence b; returns lack [1] int32 on the device: 0,
     or the free pages missing (then nothing was appended)."""
-    dev = cache._keep[0].device
-    total = k_new.shape[0]
-    _arg(k_new, "k_new", torch.bfloat16, (total, cache.Hkv, cache.D), dev)
-    _arg(v_new, "v_new", torch.bfloat16, k_new.shape, dev)
-    _arg(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
+    dev, total = cache.device, k_new.shape[0]
+    pk = _arg(k_new, "k_new", torch.bfloat16, (total, cache.Hkv, cache.D), dev)
+    pv = _arg(v_new, "v_new", torch.bfloat16, k_new.shape, dev)
+    pc = _arg(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
     with _On(k_new, stream) as st:
         lack = torch.empty(1, dtype=torch.int32, device=dev)
         if ws is None:
             ws = _workspace(pivot_cache_append_workspace_size(cache, total), dev)
-        _check(pivot_cache_append(cache, _p(k_new), _p(v_new), _p(cu_new), total, max_new, _p(lack),
-                                  _p(ws), ws.numel(), st), "pivot_cache_append")
+        _check(pivot_cache_append(cache, pk, pv, pc, total, max_new, lack.data_ptr(), _p(ws),
+                                  ws.numel(), st), "pivot_cache_append")
     return lack
 
 
 def pages_fork(cache: PivotCache, src, dst, ws=None, stream=None):
     """Make sequence dst[i] a copy of sequence src[i] as it stood before the
     call, its pages shared; src, dst [n] int32, dst distinct."""
-    dev, n = cache._keep[0].device, src.shape[0]
-    _arg(src, "src", torch.int32, (n,), dev)
-    _arg(dst, "dst", torch.int32, (n,), dev)
+    dev, n = cache.device, src.shape[0]
+    ps = _arg(src, "src", torch.int32, (n,), dev)
+    pd = _arg(dst, "dst", torch.int32, (n,), dev)
     with _On(src, stream) as st:
         if ws is None:
             ws = _workspace(pivot_pages_fork_workspace_size(cache, n), dev)
-        _check(pivot_pages_fork(cache, _p(src), _p(dst), n, _p(ws), ws.numel(), st),
+        _check(pivot_pages_fork(cache, ps, pd, n, _p(ws), ws.numel(), st),
                "pivot_pages_fork")
 
 
 def pages_free(cache: PivotCache, seqs, keep, stream=None):
     """Cut sequence seqs[i] to its first keep[i] tokens (0: free it); seqs
     distinct."""
-    dev, n = cache._keep[0].device, seqs.shape[0]
-    _arg(seqs, "seqs", torch.int32, (n,), dev)
-    _arg(keep, "keep", torch.int32, (n,), dev)
+    dev, n = cache.device, seqs.shape[0]
+    ps = _arg(seqs, "seqs", torch.int32, (n,), dev)
+    pk = _arg(keep, "keep", torch.int32, (n,), dev)
     with _On(seqs, stream) as st:
-        _check(pivot_pages_free(cache, _p(seqs), _p(keep), n, st), "pivot_pages_free")
+        _check(pivot_pages_free(cache, ps, pk, n, st), "pivot_pages_free")
 
 
 def pages_copy(src, dst, src_ids, dst_ids, stream=None):
@@ -659,20 +657,22 @@ def pages_copy(src, dst, src_ids, dst_ids, stream=None):
     dev, n = src.device, src_ids.shape[0]
     if src.dtype != dst.dtype or src.shape[1:] != dst.shape[1:]:
         raise ValueError("src and dst: pages of one type and shape")
-    _arg(src, "src", src.dtype, src.shape, dev)
-    _arg(dst, "dst", src.dtype, dst.shape, dev)
-    _arg(src_ids, "src_ids", torch.int32, (n,), dev)
-    _arg(dst_ids, "dst_ids", torch.int32, (n,), dev)
+    if not src.is_cuda or src.dim() < 1 or not src.shape[0]:
+        raise ValueError("src: pages on a CUDA device")
+    ps = _arg(src, "src", src.dtype, src.shape, dev)
+    pd = _arg(dst, "dst", src.dtype, dst.shape, dev)
+    pi = _arg(src_ids, "src_ids", torch.int32, (n,), dev)
+    pj = _arg(dst_ids, "dst_ids", torch.int32, (n,), dev)
+    page = src.numel() // src.shape[0] * src.element_size()
     with _On(src, stream) as st:
-        page = src[0].numel() * src.element_size()
-        _check(pivot_pages_copy(_p(src), src.shape[0], _p(dst), dst.shape[0], page, _p(src_ids),
-                                _p(dst_ids), n, st), "pivot_pages_copy")
+        _check(pivot_pages_copy(ps, src.shape[0], pd, dst.shape[0], page, pi, pj, n, st),
+               "pivot_pages_copy")
 
 
 def pages_compact(cache: PivotCache, ws=None, stream=None):
     """Move the pages in use to the lowest ids; returns (remap [num_pages]:
     each used page's new id, -1 for free ones; used [1])."""
-    dev = cache._keep[0].device
+    dev = cache.device
     with _On(cache._keep[0], stream) as st:
         remap = torch.empty(cache.num_pages, dtype=torch.int32, device=dev)
         used = torch.empty(1, dtype=torch.int32, device=dev)
@@ -684,30 +684,30 @@ def pages_compact(cache: PivotCache, ws=None, stream=None):
 
 
 def _attention(cache, q, cu_new, max_new, idx, scale, window, with_lse, o, ws, stream):
-    dev = cache._keep[0].device
+    dev = cache.device
+    if q.dim() != 3:
+        raise ValueError("q: [total, Hq, D]")
     total, Hq = q.shape[0], q.shape[1]
-    _arg(q, "q", torch.bfloat16, (total, Hq, cache.D), dev)
-    _arg(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
-    topk = 0
+    pq = _arg(q, "q", torch.bfloat16, (total, Hq, cache.D), dev)
+    pc = _arg(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
+    topk, pi = 0, None
     if idx is not None:
         topk = idx.shape[-1]
-        _arg(idx, "idx", torch.int32, (total, topk), dev)
-    if o is not None:
-        _arg(o, "o", torch.bfloat16, q.shape, dev)
+        pi = _arg(idx, "idx", torch.int32, (total, topk), dev)
+    po = None if o is None else _arg(o, "o", torch.bfloat16, q.shape, dev)
     name = "pivot_paged_attention" if idx is None else "pivot_selected_attention"
-    lib = load()
+    run, size = ((pivot_paged_attention, pivot_paged_attention_workspace_size) if idx is None else
+                 (pivot_selected_attention, pivot_selected_attention_workspace_size))
     with _On(q, stream) as st:
         if o is None:
             o = torch.empty_like(q)
+            po = o.data_ptr()
         lse = torch.empty(total, Hq, dtype=torch.float32, device=dev) if with_lse else None
-        call = PivotAttend(Hq, total, max_new, _p(q), _p(cu_new),
-                           cache.D ** -0.5 if scale is None else scale, window, _p(idx), topk,
-                           _p(o), _p(lse))
+        call = PivotAttend(Hq, total, max_new, pq, pc, cache.D ** -0.5 if scale is None else scale,
+                           window, pi, topk, po, None if lse is None else lse.data_ptr())
         if ws is None:
-            ws = _workspace(getattr(lib, name + "_workspace_size")(ctypes.byref(cache),
-                                                                   ctypes.byref(call)), dev)
-        _check(getattr(lib, name)(ctypes.byref(cache), ctypes.byref(call), _p(ws), ws.numel(), st),
-               name)
+            ws = _workspace(size(cache, call), dev)
+        _check(run(cache, call, _p(ws), ws.numel(), st), name)
     return o, lse
 
 
@@ -739,7 +739,7 @@ def decode_attention(batch: PivotDecode, cache: PivotCache, q, k_new, v_new, mod
     (o [B, Gm, Hq, D], lse or None, idx, lack); a lack above 0 (on the
     device) says that the pages ran out and o is not to be used."""
     B, Gm = batch.B, batch.Gm
-    dev = cache._keep[0].device
+    dev = cache.device
     if cache.B != B or tuple(q.shape[:2]) != (B, Gm):
         raise ValueError("batch, cache and q: one number of sequences and of new tokens")
     with _On(q, stream):
