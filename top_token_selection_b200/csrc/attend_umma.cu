@@ -84,14 +84,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// Whether `v` holds for any thread of a pair of warps (named barrier `id`).
-__device__ __forceinline__ bool pair_any(int id, bool v) {
+// Whether `v` holds for any of the N threads that meet at named barrier `id`.
+template <int N>
+__device__ __forceinline__ bool group_any(int id, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "r"(id)
+        : "r"((uint32_t)v), "r"(id), "n"(N)
         : "memory");
     return r != 0;
 }
@@ -205,7 +206,14 @@ struct UmmaShape {
     // per tile: which keys count, and for e4m3 their scales; selected: rows
     static constexpr int MS = 8;
     static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 12 : 0) + (SELECTED ? TKEYS * 4 : 0));
-    static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 1024 + 512;
+    static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 1024 + 512 + 2 * 48;
+};
+
+// An item as the rows warp passes it on to the others (48 bytes); n = 0: the end.
+struct Work {
+    int n, ta, b, h;            // key tiles of this CTA, the first, sequence, key/value head
+    int first, pos0, row0, rows;
+    int slot, whole, pad[2];    // partial sums' slot; all of the item's tiles are this CTA's
 };
 
 template <int D, bool FP8, bool SELECTED, bool SPLIT>
@@ -244,7 +252,10 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     uint64_t* cfull = drain + 1;                          // [CSTAGES] codes there
     uint64_t* cempty = cfull + S::CSTAGES;                // [CSTAGES] codes converted
     uint64_t* raw = cempty + S::CSTAGES;                  // V tile to be mended there
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(raw + 1);
+    uint64_t* ifull = raw + 1;                            // [2] item there
+    uint64_t* iempty = ifull + 2;                         // [2] item read
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(iempty + 2);
+    Work* m_item = reinterpret_cast<Work*>(sM + S::META + 1024 + 512);     // [2]
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -261,6 +272,10 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             bar_init(&mempty[i], (SPLIT ? 8 : 16) + (FP8 ? COPY_WARPS : 0));
         }
         bar_init(raw, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&ifull[i], 1);
+            bar_init(&iempty[i], S::WARPS - 1);
+        }
         for (int i = 0; i < 2; ++i) {
             bar_init(&sfull[i], 1);
             bar_init(&pfull[2 * i], 4);
@@ -291,6 +306,26 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     const long long u_begin = used ? run_begin(units, blockIdx.x, ncta) : 0;
     const long long u_end = used ? run_begin(units, blockIdx.x + 1, ncta) : 0;
 
+    // The next item, from the rows warp (one descriptor read of dependent loads
+    // costs some 5000 cycles); false if it never came.
+    uint32_t i_at = 0, i_ph = 0;
+    auto next_item = [&](Work& w) -> bool {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(&ifull[i_at], i_ph));
+        if (!got) return false;
+        const int4* from = reinterpret_cast<const int4*>(&m_item[i_at]);
+        const int4 a = from[0], b = from[1], c = from[2];
+        w.n = a.x; w.ta = a.y; w.b = a.z; w.h = a.w;
+        w.first = b.x; w.pos0 = b.y; w.row0 = b.z; w.rows = b.w;
+        w.slot = c.x; w.whole = c.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&iempty[i_at]);
+        if (++i_at == 2) {
+            i_at = 0;
+            i_ph ^= 1;
+        }
+        return true;
+    };
+
     if (warp == LOAD_WARP) {
         // ------------------------------------------------------- rows, loads
         // A lane looks after keys 4 lane .. 4 lane + 3 of a tile: their
@@ -307,6 +342,22 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
         const int box = min(TKEYS, p.c.page_size());           // keys of a TMA box
         const int boxes = TKEYS / box;
         if (u_begin == u_end && lane == 0) p.join[blockIdx.x].rows = 0;
+        auto pass_on = [&](const Work& w) -> bool {
+            if (!__all_sync(0xffffffffu, mbar_wait(&iempty[i_at], i_ph ^ 1))) return false;
+            if (lane == 0) {
+                int4* to = reinterpret_cast<int4*>(&m_item[i_at]);
+                to[0] = make_int4(w.n, w.ta, w.b, w.h);
+                to[1] = make_int4(w.first, w.pos0, w.row0, w.rows);
+                to[2] = make_int4(w.slot, w.whole, 0, 0);
+                mbar_arrive(&ifull[i_at]);
+            }
+            __syncwarp();
+            if (++i_at == 2) {
+                i_at = 0;
+                i_ph ^= 1;
+            }
+            return true;
+        };
         for (long long u = u_begin; u < u_end && !aborted;) {
             const Item it = find_item<SELECTED>(p, u);
             const int ta = it.tile0 + (int)(u - it.unit0);
@@ -314,6 +365,12 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             if (u == u_begin && lane == 0) put_join(p, it, units, u_begin, blockIdx.x, ncta);
             u = it.unit0 + (tz - it.tile0);
             if (!it.ok) continue;
+            if (!pass_on(Work{tz - ta, ta, it.b, it.h, it.first, it.pos0, it.row0, it.rows,
+                              2 * (int)blockIdx.x + (it.unit0 < u_begin ? 0 : 1),
+                              it.unit0 >= u_begin && it.unit0 + it.tiles <= u_end, {0, 0}})) {
+                aborted = true;
+                break;
+            }
             const int lim_lo = it.pos0 + it.row0 / p.G;
             const int lim_hi = it.pos0 + (it.row0 + it.rows - 1) / p.G;
             const int key_lo = p.window ? max(0, lim_lo - p.window + 1) : 0;
@@ -474,6 +531,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                 }
             }
         }
+        if (!aborted) pass_on(Work{});
         // every load has landed before the CTA may end
         for (uint32_t i = 0; i < RING && i < loaded; ++i) {
             const uint32_t e = loaded - 1 - i;
@@ -518,13 +576,9 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     phase ^= 1;
                 }
             };
-            for (long long u = u_begin; u < u_end && !aborted;) {
-                const Item it = find_item<SELECTED>(p, u);
-                const int ta = it.tile0 + (int)(u - it.unit0);
-                const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
-                u = it.unit0 + (tz - it.tile0);
-                if (!it.ok) continue;
-                const int total = 2 * (tz - ta);               // K and V tiles of the item
+            Work it;
+            while (!aborted && next_item(it) && it.n > 0) {
+                const int total = 2 * it.n;                    // K and V tiles of the item
                 const size_t head_off = (size_t)it.h * D * es + ch * 16;
                 // copies of tile x (K if even) towards shared memory at dst(k)
                 auto copy = [&](int x, auto dst) -> bool {
@@ -688,13 +742,9 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             if (SPLIT || t == 1) next(ks, kph);
             return true;
         };
-        for (long long u = u_begin; u < u_end && !aborted;) {
-            const Item it = find_item<SELECTED>(p, u);
-            const int ta = it.tile0 + (int)(u - it.unit0);
-            const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
-            u = it.unit0 + (tz - it.tile0);
-            if (!it.ok) continue;
-            const int n = __shfl_sync(0xffffffffu, tz - ta, 0), H = SPLIT ? n : 2 * n;
+        Work it;
+        while (!aborted && next_item(it) && it.n > 0) {
+            const int n = __shfl_sync(0xffffffffu, it.n, 0), H = SPLIT ? n : 2 * n;
             if (!mbar_wait(qfull, qph)) break;
             qph ^= 1;
             tc_fence_after();
@@ -745,16 +795,46 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
         uint32_t sph = 0, oph[2] = {0, 0};
         int tile_no = 0;
         bool aborted = false;
-        for (long long u = u_begin; u < u_end;) {
-            const Item it = find_item<SELECTED>(p, u);
-            const int ta = it.tile0 + (int)(u - it.unit0);
-            const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
-            const bool whole = it.unit0 >= u_begin && it.unit0 + it.tiles <= u_end;
-            const int slot = 2 * blockIdx.x + (it.unit0 < u_begin ? 0 : 1);
-            u = it.unit0 + (tz - it.tile0);
-            if (!it.ok) continue;
-            const int n = tz - ta;
+        // All warps of a stream (split: of both) go on or stop together, since
+        // they meet at named barriers.
+        Work it;
+        auto fetch = [&]() -> bool {
+            const bool lost = !next_item(it);
+            if (SPLIT ? group_any<SOFT_WARPS * 32>(9, lost) : group_any<64>(pair, lost)) return false;
+            return it.n > 0;
+        };
+        // this thread's half of its query row (e4m3: and the row's largest
+        // value) is read while the item before ends
+        uint4 qh[D / 16];
+        float amax = 0.0f;
+        auto read_q = [&]() {
+            const int rr = it.row0 + rb;
             const bool live = rb < it.rows;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.q + (live ? (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G : 0) * D);
+            amax = 0.0f;
+            if constexpr (FP8) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 q = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
+                                                 fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+                }
+            }
+            if (!SPLIT || t == 0) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    qh[k] = live ? __ldg(src + x * (D / 16) + k) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        bool more = fetch();
+        if (more) read_q();
+        while (more) {
+            const int n = it.n, ta = it.ta, slot = it.slot;
+            const bool whole = it.whole != 0, live = rb < it.rows;
             const int rr = it.row0 + rb;
             const size_t head = live ? (size_t)(it.first + rr / p.G) * p.Hq + it.h * p.G + rr % p.G : 0;
             const int lim = live ? it.pos0 + rr / p.G : -1;
@@ -766,19 +846,8 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             // row's largest value)
             float c = p.scale_log2;
             {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + head * D);
                 float down = 1.0f;
                 if constexpr (FP8) {
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 q = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)),
-                                                     fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
-                    }
                     const uint32_t e = __float_as_uint(amax) & 0x7F800000u;
                     if (e > 0x01000000u && e < 0x7E000000u) {
                         c *= __uint_as_float(e);
@@ -790,8 +859,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const int i = x * (D / 16) + k;
-                        const uint4 q = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                        uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                        uint32_t w[4] = {qh[k].x, qh[k].y, qh[k].z, qh[k].w};
                         if constexpr (FP8) {
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
@@ -867,7 +935,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     // e4m3: without the rest of the scales, up to 2^-7 off
                     if (FP8 && top > -INFINITY) top += fabsf(top - lv) * 0.0078125f;
                 }
-                if (pair_any(pair, top > m + LAG)) {
+                if (group_any<64>(pair, top > m + LAG)) {
                     atomicMax(&m_top[t * 128 + r], ordered_key(top));
                     named_bar_sync(pair, 64);
                     top = key_to_float(m_top[t * 128 + r]);
@@ -927,6 +995,8 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             tile_no += n;
 
             // ---- the item's end
+            more = fetch();
+            if (more) read_q();
             if (!aborted) {
                 bool got = true;
 #pragma unroll
