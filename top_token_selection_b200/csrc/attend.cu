@@ -231,13 +231,11 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                                              fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
 #pragma unroll
                 for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-                const uint32_t e = __float_as_uint(amax) & 0x7F800000u;
-                float down = 1.0f, up = 1.0f;
-                if (e > 0x01000000u && e < 0x7E000000u) {        // 2^e and 2^-e are normal
-                    up = __uint_as_float(e);
-                    down = __uint_as_float(0x7F000000u - e);
-                }
-                mul *= up;
+                // within [2^-125, 2^124]: 2^e and 2^-e are normal
+                const uint32_t e =
+                    min(max(__float_as_uint(amax) & 0x7F800000u, 0x01000000u), 0x7D800000u);
+                const float down = __uint_as_float(0x7F000000u - e);
+                mul *= __uint_as_float(e);
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
                     x[i] = f16x2(__uint_as_float(x[i] << 16) * down,

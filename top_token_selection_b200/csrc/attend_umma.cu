@@ -206,7 +206,7 @@ struct UmmaShape {
     // per tile: which keys count, and for e4m3 their scales; selected: rows
     static constexpr int MS = 8;
     static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 12 : 0) + (SELECTED ? TKEYS * 4 : 0));
-    static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 1024 + 512 + 2 * 48;
+    static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 1024 + 512 + 2 * 48 + TKEYS;
 };
 
 // An item as the rows warp passes it on to the others (48 bytes); n = 0: the end.
@@ -256,6 +256,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     uint64_t* iempty = ifull + 2;                         // [2] item read
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(iempty + 2);
     Work* m_item = reinterpret_cast<Work*>(sM + S::META + 1024 + 512);     // [2]
+    float* m_one = reinterpret_cast<float*>(m_item + 2);  // [32] of 1
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -288,6 +289,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
     }
+    if (warp == 1) m_one[lane] = 1.0f;
     __syncwarp();
     if (warp == MMA_WARP) {
         tmem_alloc(tmem_at, 512);
@@ -848,11 +850,10 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             {
                 float down = 1.0f;
                 if constexpr (FP8) {
-                    const uint32_t e = __float_as_uint(amax) & 0x7F800000u;
-                    if (e > 0x01000000u && e < 0x7E000000u) {
-                        c *= __uint_as_float(e);
-                        down = __uint_as_float(0x7F000000u - e);
-                    }
+                    const uint32_t e =
+                        min(max(__float_as_uint(amax) & 0x7F800000u, 0x01000000u), 0x7D800000u);
+                    c *= __uint_as_float(e);
+                    down = __uint_as_float(0x7F000000u - e);
                 }
                 if (!SPLIT || t == 0) {
                     const uint32_t dst = smem_u32(sQ) + (SPLIT ? 0 : t * S::TILE);
@@ -891,16 +892,21 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                 const int key0 = (ta + j) * TKEYS + 64 * x;
                 const bool plain = (ok.x & ok.y) == 0xffffffffu &&
                                    (SELECTED || (key0 + 63 <= lim_lo && (!p.window || key0 > lim_hi - p.window)));
+                // which of 32 keys count for this row
+                auto seen = [&](int i) -> uint32_t {
+                    if (plain) return 0xffffffffu;
+                    // keys from..to of these 64 are this row's
+                    const int to = SELECTED ? 63 : lim - key0;
+                    const int from = !SELECTED && p.window ? lim - p.window + 1 - key0 : 0;
+                    const int a = min(max(from - 32 * i, 0), 32), z = min(max(to - 32 * i + 1, 0), 32);
+                    const uint32_t below = z == 32 ? 0xffffffffu : (1u << z) - 1;
+                    const uint32_t above = a == 32 ? 0u : 0xffffffffu << a;
+                    return (i ? ok.y : ok.x) & below & above;
+                };
                 // the scores of keys that do not count
                 auto finish = [&](float* s, int i) {
                     if (!plain) {
-                        // keys from..to of these 64 are this row's
-                        const int to = SELECTED ? 63 : lim - key0;
-                        const int from = !SELECTED && p.window ? lim - p.window + 1 - key0 : 0;
-                        const int a = min(max(from - 32 * i, 0), 32), z = min(max(to - 32 * i + 1, 0), 32);
-                        const uint32_t below = z == 32 ? 0xffffffffu : (1u << z) - 1;
-                        const uint32_t above = a == 32 ? 0u : 0xffffffffu << a;
-                        const uint32_t see = (i ? ok.y : ok.x) & below & above;
+                        const uint32_t see = seen(i);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1 ? s[k] : -INFINITY;
                     }
@@ -914,9 +920,8 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                 // The reference point may lag behind the maximum by LAG:
                 // weights then reach 2^LAG, which costs no precision (bf16 has
                 // the exponents of fp32; f16 ends at 2^16), and m and the sums
-                // in TMEM seldom have to move (with a lag of 8 a move, which
-                // takes about 900 cycles, came in every other tile of rows
-                // with a few heavy keys).  For e4m3 m stands over the weights
+                // in TMEM seldom have to move (2048 new tokens over 32K, bf16:
+                // 1147 us with a lag of 8, 1088 with 64).  For e4m3 m stands over the weights
                 // times the values' scales, so that their product fits f16
                 // whatever the scales; the sums of both are in its units,
                 // which cancel in o.
@@ -932,8 +937,32 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                         largest(a, mx);
                     }
                     top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * ct + lv;
-                    // e4m3: without the rest of the scales, up to 2^-7 off
-                    if (FP8 && top > -INFINITY) top += fabsf(top - lv) * 0.0078125f;
+                }
+                // Scores whose fp32 rounding (e4m3: the rest of their scales,
+                // within 2^-7 of 1) is no longer small beside 1 are rounded
+                // before the reference point is taken and subtracted, so that
+                // the largest weight is 1 however large they are.
+                const bool far = __any_sync(
+                    0xffffffffu, top > -INFINITY && fabsf(top - lv) > (FP8 ? 512.0f : 1048576.0f));
+                const float* rest = m_rest + ms * TKEYS + 64 * x;
+                if constexpr (FP8) {
+                    if (!far) {
+                        if (top > -INFINITY) top += fabsf(top - lv) * 0.0078125f;
+                    } else if (!aborted) {
+                        top = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t b[16];
+                            tmem_ld16(tS + 64 * x + 16 * i, b);
+                            tmem_ld_wait();
+                            const uint32_t see = seen(i >> 1) >> (16 * (i & 1));
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                if ((see >> k) & 1)
+                                    top = fmaxf(top, __fadd_rn(__fmul_rn(__uint_as_float(b[k]),
+                                                                         __fmul_rn(ct, rest[16 * i + k])), lv));
+                        }
+                    }
                 }
                 if (group_any<64>(pair, top > m + LAG)) {
                     atomicMax(&m_top[t * 128 + r], ordered_key(top));
@@ -963,7 +992,23 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     named_bar_sync(pair, 64);      // all of the row's sums have moved
                 }
                 if (aborted) continue;
-                const float z = m == -INFINITY ? 0.0f : lv - m;
+                if (far) {
+                    const float m0 = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t b[16];
+                        tmem_ld16(tS + 64 * x + 16 * i, b);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float f = FP8 ? __fmul_rn(ct, rest[16 * i + k]) : ct;
+                            b[k] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(b[k]), f), lv) - m0);
+                        }
+                        tmem_st16(tS + 64 * x + 16 * i, b);
+                    }
+                    tmem_st_wait();
+                }
+                const float z = far || m == -INFINITY ? 0.0f : lv - m, cw = far ? 1.0f : ct;
                 begun = true;
                 // P takes the place of these 64 keys' S, half of it at a time:
                 // the scores are read again, for all 64 would not fit in the
@@ -974,11 +1019,11 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     tmem_ld32(tS + 64 * x, a);
                     tmem_ld_wait();
                     finish(a, 0);
-                    weights<FP8>(a, ct, z, m_rest + ms * TKEYS + 64 * x, tS + 64 * x, sum);
+                    weights<FP8>(a, cw, z, far ? m_one : rest, tS + 64 * x, sum);
                     tmem_ld32(tS + 64 * x + 32, a);
                     tmem_ld_wait();
                     finish(a, 1);
-                    weights<FP8>(a, ct, z, m_rest + ms * TKEYS + 64 * x + 32, tS + 64 * x + 16, sum);
+                    weights<FP8>(a, cw, z, far ? m_one : rest + 32, tS + 64 * x + 16, sum);
                     float s0, s1, s2, s3;
                     unpack2(sum[0], s0, s1);
                     unpack2(sum[1], s2, s3);
