@@ -223,7 +223,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     using S = UmmaShape<D, FP8, SELECTED, SPLIT>;
     constexpr int STAGES = S::STAGES, MS = S::MS;
     constexpr int R = SPLIT ? 128 : 256;
-    constexpr float LAG = FP8 ? 14.0f : 64.0f;
+    constexpr float LAG = FP8 ? 14.0f : 64.0f, FAR = FP8 ? 512.0f : 1048576.0f;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -878,6 +878,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             float m = -INFINITY, l = 0.0f;                 // l: of this thread's keys
             if (x == 0) m_top[t * 128 + r] = 0;            // below every number; read after a barrier
             bool begun = false;                            // O holds sums
+            bool far = false;                              // |m| > FAR in some row of the warp
             for (int j = SPLIT ? t : 0; j < n; j += SPLIT ? 2 : 1) {
                 const int ms = (tile_no + j) % MS;
                 if (!aborted) {
@@ -921,10 +922,10 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                 // weights then reach 2^LAG, which costs no precision (bf16 has
                 // the exponents of fp32; f16 ends at 2^16), and m and the sums
                 // in TMEM seldom have to move (2048 new tokens over 32K, bf16:
-                // 1147 us with a lag of 8, 1088 with 64).  For e4m3 m stands over the weights
-                // times the values' scales, so that their product fits f16
-                // whatever the scales; the sums of both are in its units,
-                // which cancel in o.
+                // 1147 us with a lag of 8, 1088 with 64).  For e4m3 m stands
+                // over the weights times the values' scales, so that their
+                // product fits f16 whatever the scales; the sums of both are
+                // in its units, which cancel in o.
                 float top = -INFINITY;
                 if (!aborted) {
                     float a[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -937,34 +938,28 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                         largest(a, mx);
                     }
                     top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * ct + lv;
+                    // e4m3: without the rest of the scales, up to 2^-7 off
+                    if (FP8 && top > -INFINITY) top += fabsf(top - lv) * 0.0078125f;
                 }
-                // Scores whose fp32 rounding (e4m3: the rest of their scales,
-                // within 2^-7 of 1) is no longer small beside 1 are rounded
-                // before the reference point is taken and subtracted, so that
-                // the largest weight is 1 however large they are.
-                const bool far = __any_sync(
-                    0xffffffffu, top > -INFINITY && fabsf(top - lv) > (FP8 ? 512.0f : 1048576.0f));
                 const float* rest = m_rest + ms * TKEYS + 64 * x;
-                if constexpr (FP8) {
-                    if (!far) {
-                        if (top > -INFINITY) top += fabsf(top - lv) * 0.0078125f;
-                    } else if (!aborted) {
-                        top = -INFINITY;
+                if (group_any<64>(pair, top > m + LAG)) {
+                    if constexpr (FP8) {
+                        if (__any_sync(0xffffffffu, fabsf(top) > FAR && top > -INFINITY) && !aborted) {
+                            top = -INFINITY;               // with the rest of the scales
 #pragma unroll 1
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t b[16];
-                            tmem_ld16(tS + 64 * x + 16 * i, b);
-                            tmem_ld_wait();
-                            const uint32_t see = seen(i >> 1) >> (16 * (i & 1));
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t b[16];
+                                tmem_ld16(tS + 64 * x + 16 * i, b);
+                                tmem_ld_wait();
+                                const uint32_t see = seen(i >> 1) >> (16 * (i & 1));
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if ((see >> k) & 1)
-                                    top = fmaxf(top, __fadd_rn(__fmul_rn(__uint_as_float(b[k]),
-                                                                         __fmul_rn(ct, rest[16 * i + k])), lv));
+                                for (int k = 0; k < 16; ++k)
+                                    if ((see >> k) & 1)
+                                        top = fmaxf(top, __fadd_rn(__fmul_rn(__uint_as_float(b[k]),
+                                                                             __fmul_rn(ct, rest[16 * i + k])), lv));
+                            }
                         }
                     }
-                }
-                if (group_any<64>(pair, top > m + LAG)) {
                     atomicMax(&m_top[t * 128 + r], ordered_key(top));
                     named_bar_sync(pair, 64);
                     top = key_to_float(m_top[t * 128 + r]);
@@ -974,6 +969,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                         m = top;
                     }
                     l *= f;
+                    far = __any_sync(0xffffffffu, fabsf(m) > FAR && m > -INFINITY);
                     // the product that wrote O was complete before this S was;
                     // each warp takes half of the values
                     if (begun && !aborted) {
@@ -992,6 +988,11 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     named_bar_sync(pair, 64);      // all of the row's sums have moved
                 }
                 if (aborted) continue;
+                // Beside a reference point that fp32 holds no longer to a small
+                // part of 1 (e4m3: where 2^-7 of it, for the rest of the
+                // scales, is not small) the scores are rounded as its were
+                // before it is subtracted: the largest weight is about 1
+                // however large they are.
                 if (far) {
                     const float m0 = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
