@@ -350,13 +350,14 @@ pivot_status_t pivot_decode_noalloc(const pivot_decode_t* batch, int32_t mode, i
  * can be captured into a graph and replayed.
  *   page_size 16, 32, 64, 128 or 256; num_pages * page_size < 2^31;
  *   1 <= B <= 65536; D * (bytes of a value) a multiple of 16 (attention:
- *   D = 64 or 128); k, v 16-byte aligned.
+ *   D = 64 or 128, max_pages * page_size <= 2^26); k, v 16-byte aligned.
  * What the host cannot check sets the error word (PIVOT_ERR_DEVICE).  Row
  * offsets, sequence ids, counts or lengths out of range: the append and the
  * page calls then change nothing, and attention leaves the rows of that
  * sequence unwritten.  A page id out of range: the append changes nothing,
  * the other page calls pass over that table entry, and attention counts the
- * page's tokens as masked. */
+ * page's tokens as masked (selected: rows whose own token lies on it may stay
+ * unwritten). */
 typedef struct {
     int32_t dtype;               /* PIVOT_BF16 or PIVOT_E4M3                     */
     int32_t B, Hkv, D;           /* sequences, key/value heads, head dim         */
@@ -440,20 +441,24 @@ size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
  * [0, p] (-1 padding) left out; an entry named twice counts twice.  idx rows
  * are what the indexer's calls write, in either order.
  * Slots past a sequence's tokens may hold anything; the tokens' own stored
- * keys and values are finite.  Rows of o and lse from cu_new[B] on stay as
- * they were.  Products run on the tensor cores with fp32
- * sums, and the softmax in fp32.  Rounded are the weights of the product with
- * V: to bf16 beside bf16 values; to f16 beside e4m3 codes, which go into the
- * products exactly, as f16, with their scales in fp32 (a value whose scale
- * is below 2^-14 of the largest of its tile of 32 to 128 tokens loses bits).
- * scale: any positive finite value. */
+ * keys and values are finite (e4m3: scales of at most 2^100).  Rows of o and
+ * lse from cu_new[B] on stay as they were.
+ * Products run on the tensor cores with fp32 sums, and the softmax and its
+ * sums in fp32.  The weights of the product with V are rounded: to bf16
+ * beside bf16 values, to f16 beside e4m3 ones.  e4m3 codes go into the
+ * products as f16.  With up to 32 query rows a key they go in exactly and
+ * their scales stay in fp32; with more, a key's scale is split into 7 bits that
+ * go in with the code, exactly, and a rest in fp32, and a value's scale and
+ * its product with the code are rounded to f16 (2^-12 each).  A value whose
+ * scale is below 2^-14 of the largest of its tile of 32 to 128 tokens loses
+ * bits, and so does, with more than 32 rows, such a key. */
 typedef struct {
     int32_t Hq;                  /* query heads, a multiple of Hkv               */
     int32_t total;               /* rows of q                                    */
     int32_t max_new;             /* at least every sequence's count              */
     const void* q;               /* bf16 [total, Hq, D], 16-byte aligned         */
     const int32_t* cu_new;       /* [B + 1] on the device                        */
-    float scale;
+    float scale;                 /* above 0, at most 1e30                        */
     int32_t window;              /* 0: the whole prefix (selected: must be 0)    */
     const int32_t* idx;          /* [total, topk] (paged: NULL)                  */
     int32_t topk;                /* 1 .. 65536 (paged: 0)                        */

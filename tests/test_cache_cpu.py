@@ -83,6 +83,8 @@ def test_attention_refuses_more():
     assert pv.pivot_selected_attention(c, call(idx=FAKE, topk=4, window=3), *WS, None) == 1
     assert pv.pivot_selected_attention(c, call(idx=FAKE, topk=65537), *WS, None) == 2
     assert pv.pivot_paged_attention(cache(D=32), call(), *WS, None) == 2
+    assert pv.pivot_paged_attention(c, call(scale=2e30), *WS, None) == 1
+    assert pv.pivot_paged_attention(cache(max_pages=(1 << 22) + 1), call(), *WS, None) == 2
     assert pv.pivot_paged_attention(cache(D=256), call(), *WS, None) == 2
     assert pv.pivot_paged_attention(c, call(), None, 1 << 40, None) == 1
     assert pv.pivot_paged_attention(c, call(), FAKE + 16, 1 << 40, None) == 1

@@ -260,3 +260,101 @@ def test_scores_of_every_size(D, fp8, n, Hq, topk):
     agree(tuple(x[:, 2:] for x in got), tuple(x[:, 2:] for x in want))
     assert float(((got[0].double() - want[0]).abs()[:, :2] / want[2][:, :2]).max()) < 2 ** -6
     assert float((got[1].double() / want[1] - 1).abs()[:, :2].max()) < 2 ** -16
+
+
+@pytest.mark.parametrize("length", [-100, -1, 14 * 16 + 1, 2 ** 31 - 1])
+def test_lengths_out_of_range_change_nothing(length):
+    c, _ = fill([200, 150, 170], 16, 1, 64, False, seed=13)
+    assert c.table.shape[1] == 14
+    c.refs[c.table[c.table >= 0].long()] = 1
+    c.len[1] = length
+    before = [t.clone() for t in (c.table, c.len, c.refs)]
+    pv.pages_free(c.c, i32([0, 1]), i32([3, 0]))
+    assert pv.device_error() == 6
+    pv.pages_fork(c.c, i32([1, 0]), i32([0, 2]))
+    assert pv.device_error() == 6
+    for a, b in zip(before, (c.table, c.len, c.refs)):
+        assert torch.equal(a, b)
+    pv.pages_fork(c.c, i32([0]), i32([1]))           # a sequence is mended by becoming another
+    assert pv.device_error() == 0 and int(c.len[1]) == 200
+
+
+@pytest.mark.parametrize("n,Hq,topk", [(2, 4, 0), (70, 8, 0), (3, 4, 150), (3, 80, 150)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_past_4_gib_of_a_plane(fp8, n, Hq, topk):
+    # the same tokens at the pool's beginning and behind 2^32 bytes of it
+    # give the same bits
+    Hkv, D, page = (4, 128, 64) if Hq < 80 else (1, 128, 64)
+    Hq *= Hkv
+    small, gen = fill([300], page, Hkv, D, fp8, seed=14)
+    pages = (2 ** 32 + 2 ** 27) // (page * Hkv * D * (1 if fp8 else 2))
+    k, v = (torch.empty(pages, *small.k.shape[1:], dtype=small.k.dtype, device=DEV) for _ in range(2))
+    ks, vs = (torch.empty(pages, page, device=DEV) for _ in range(2)) if fp8 else (None, None)
+    refs = torch.zeros(pages, dtype=torch.int32, device=DEV)
+    far = torch.arange(pages - 5, pages, dtype=torch.int32, device=DEV)
+    near = small.table[0, :5].contiguous()
+    for a, b in ((small.k, k), (small.v, v)):
+        pv.pages_copy(a, b, near, far)
+        if fp8:
+            assert torch.equal(a.view(torch.uint8)[near.long()], b[-5:].view(torch.uint8))
+    if fp8:
+        ks[-5:], vs[-5:] = small.ks[near.long()], small.vs[near.long()]
+    refs[-5:] = 1
+    c = pv.make_cache(k, v, far[None].contiguous(), small.len.clone(), refs, ks, vs)
+    q = torch.randn(n, Hq, D, generator=gen).to(torch.bfloat16).to(DEV)
+    cu = offsets([n])
+    if topk:
+        idx = torch.randint(-1, 290, (n, topk), generator=gen, dtype=torch.int32).to(DEV)
+        def run(x): return pv.selected_attention(x, q, cu, n, idx, with_lse=True)
+    else:
+        def run(x): return pv.paged_attention(x, q, cu, n, with_lse=True)
+    want, got = run(small.c), run(c)
+    remap, used = pv.pages_compact(c)
+    after = run(c)
+    assert pv.device_error() == 0 and int(used) == 5
+    assert torch.equal(remap[-5:].cpu(), torch.arange(5, dtype=torch.int32))
+    for a, b, d in zip(want, got, after):
+        assert torch.equal(a, b) and torch.equal(a, d)
+
+
+@pytest.mark.parametrize("G", [1, 4, 20])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_short_sequences(fp8, G):
+    B = 2500
+    gen = torch.Generator().manual_seed(15)
+    c = Cache(B, 2, 2 * B, 16, 1, 64, fp8)
+    n0 = torch.randint(0, 25, (B,), generator=gen).tolist()
+    n1 = [int(x) if int(x) else 0 for x in torch.randint(0, 4, (B,), generator=gen)]
+    c.append(n0, gen)
+    c.append(n1, gen)
+    c.check()
+    total = sum(n1)
+    q = torch.randn(total, G, 64, generator=gen).to(torch.bfloat16).to(DEV)
+    agree(pv.paged_attention(c.c, q, offsets(n1), 3, with_lse=True), expected(c, q, n1, c.model.len))
+    idx = torch.randint(-1, 30, (total, 20), generator=gen, dtype=torch.int32).to(DEV)
+    agree(pv.selected_attention(c.c, q, offsets(n1), 3, idx, with_lse=True),
+          expected(c, q, n1, c.model.len, idx=idx))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hq", [4, 40])
+def test_a_bad_own_page_beside_garbage(Hq, fp8):
+    # the first row of the pool is no number; the first of three new tokens is
+    # on a good page, the others' own is gone: they are right or unwritten
+    c, gen = fill([194], 16, 1, 64, fp8, seed=16)
+    assert not bool((c.table == 0).any())
+    q = torch.randn(3, Hq, 64, generator=gen).to(torch.bfloat16).to(DEV)
+    idx = torch.full((3, 90), -1, dtype=torch.int32, device=DEV)
+    idx[:, :50] = torch.arange(30, 80, device=DEV)
+    ow, lw, size = expected(c, q, [3], [194], idx=idx)
+    c.table[0, 12] = -1
+    for plane in (c.k, c.v):
+        plane.view(torch.uint8)[0] = 0x7F if fp8 else 0xFF
+    o = torch.full_like(q, 3.5)
+    _, lse = pv.selected_attention(c.c, q, offsets([3]), 3, idx, o=o, with_lse=True)
+    assert pv.device_error() == (0 if Hq == 4 else 6)
+    agree((o[:1], lse[:1]), (ow[:1], lw[:1], size[:1]))
+    if Hq == 4:
+        agree((o, lse), (ow, lw, size))
+    else:
+        assert bool((o[1:] == 3.5).all())

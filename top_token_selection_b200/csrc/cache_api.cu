@@ -1,7 +1,6 @@
 // cache_api.cu -- C entry points of the paged cache: argument checks,
 // workspace layout and launches.  See include/pivot.h for the contract.
 #include <climits>
-#include <cmath>
 
 #include "attend.h"
 #include "host.h"
@@ -17,6 +16,7 @@ namespace {
 constexpr size_t WS_ALIGN = 256;
 constexpr int MAX_SEQS = 65536;      // sequence ids are marked in one bit each of shared memory
 constexpr int MAX_SELECTED = 65536;
+constexpr int MAX_TOKENS = 1 << 26;  // the plan counts 1024 row blocks' tiles of 64 tokens in 32 bits
 
 struct Range {
     explicit Range(const char* name) { nvtxRangePushA(name); }
@@ -69,13 +69,15 @@ pivot_status_t check_attend(const pivot_cache_t* cache, const pivot_attend_t* a,
     if (st != PIVOT_OK) return st;
     if (!a || a->Hq < 1 || a->total < 0 || a->max_new < 0 || a->window < 0) return PIVOT_ERR_INVALID_ARG;
     if (a->Hq % cache->Hkv) return PIVOT_ERR_INVALID_ARG;
-    if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return PIVOT_ERR_INVALID_ARG;
+    if (!(a->scale > 0.0f) || !(a->scale <= 1e30f)) return PIVOT_ERR_INVALID_ARG;
     if (selected ? (a->topk < 1 || a->window != 0) : (a->topk != 0 || a->idx)) return PIVOT_ERR_INVALID_ARG;
     if (a->total > 0 && (!a->q || !a->cu_new || !a->o || a->max_new < 1 || (selected && !a->idx)))
         return PIVOT_ERR_INVALID_ARG;
     if (!aligned(a->q, 16) || !aligned(a->o, 16)) return PIVOT_ERR_INVALID_ARG;
     if (cache->D != 64 && cache->D != 128) return PIVOT_ERR_UNSUPPORTED;
-    if (a->topk > MAX_SELECTED || (long long)a->total * a->Hq > INT_MAX) return PIVOT_ERR_UNSUPPORTED;
+    if (a->topk > MAX_SELECTED || (long long)a->total * a->Hq > INT_MAX ||
+        (long long)cache->max_pages * cache->page_size > MAX_TOKENS)
+        return PIVOT_ERR_UNSUPPORTED;
     p->q = static_cast<const uint16_t*>(a->q);
     p->cu = a->cu_new;
     p->idx = selected ? a->idx : nullptr;

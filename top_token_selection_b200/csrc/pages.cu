@@ -228,15 +228,19 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Whether the n sequence ids are in range and (distinct) each named once; all
-// threads of the block get the verdict.  seen: B bits of shared memory.
-__device__ bool ids_ok(const int32_t* ids, int n, int B, bool distinct, uint32_t* seen) {
+// Whether the n sequence ids and (lengths) those sequences' lengths are in
+// range, and (distinct) each is named once; all threads of the block get the
+// verdict, the same in every block: a length that another block has changed
+// was in range and still is.  seen: B bits of shared memory.
+__device__ bool ids_ok(const CacheView& c, const int32_t* ids, int n, bool distinct, bool lengths, uint32_t* seen) {
+    const int B = c.B, most = c.max_pages << c.page_log2;
     for (int i = threadIdx.x; i < (B + 31) / 32; i += blockDim.x) seen[i] = 0;
     __syncthreads();
     bool ok = true;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int b = ids[i];
         if ((unsigned)b >= (unsigned)B) ok = false;
+        else if (lengths && (unsigned)c.len[b] > (unsigned)most) ok = false;
         else if (distinct && (atomicOr(&seen[b >> 5], 1u << (b & 31)) >> (b & 31)) & 1u) ok = false;
     }
     return __syncthreads_and(ok);
@@ -246,7 +250,7 @@ __device__ bool ids_ok(const int32_t* ids, int n, int B, bool distinct, uint32_t
 __global__ void __launch_bounds__(1024)
     fork_take_kernel(const CacheView c, const int32_t* src, const int32_t* dst, int n, int32_t* ws) {
     extern __shared__ uint32_t seen[];
-    if (!ids_ok(dst, n, c.B, true, seen) || !ids_ok(src, n, c.B, false, seen)) {
+    if (!ids_ok(c, dst, n, true, false, seen) || !ids_ok(c, src, n, false, true, seen)) {
         if (threadIdx.x == 0) raise_error(ERRBIT_DATA);
         return;
     }
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(1024)
     fork_give_kernel(const CacheView c, const int32_t* src, const int32_t* dst, int n,
                      const int32_t* ws) {
     extern __shared__ uint32_t seen[];
-    if (!ids_ok(dst, n, c.B, true, seen) || !ids_ok(src, n, c.B, false, seen)) return;
+    if (!ids_ok(c, dst, n, true, false, seen) || !ids_ok(c, src, n, false, true, seen)) return;
     const int i = blockIdx.x, d = dst[i];
     const int32_t* row = ws + n + (size_t)i * c.max_pages;
     int32_t* to = c.table + (size_t)d * c.max_pages;
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(1024)
 __global__ void __launch_bounds__(1024)
     free_kernel(const CacheView c, const int32_t* seqs, const int32_t* keep, int n) {
     extern __shared__ uint32_t seen[];
-    bool ok = ids_ok(seqs, n, c.B, true, seen);
+    bool ok = ids_ok(c, seqs, n, true, true, seen);
     bool neg = false;
     for (int i = threadIdx.x; i < n; i += blockDim.x) neg |= keep[i] < 0;
     ok = !__syncthreads_or(neg) && ok;
