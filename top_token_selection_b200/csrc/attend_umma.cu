@@ -26,9 +26,15 @@
 // What bounds it: the products.  On one SM a 128 x 128 x 16 product takes 96
 // cycles with both operands in shared memory and 75 with P in TMEM (64 would
 // be the nominal rate; measured back to back), 103 when the two alternate:
-// about 3300 cycles for 256 rows x 128 keys at D = 128.  The kernel takes
-// about 4250: a tile's softmax waits for its S, which waits for its last
-// product with V, and only two tiles fit into TMEM to fill the gap.
+// about 3300 cycles for 256 rows x 128 keys at D = 128.  2048 new tokens over
+// 32K (bf16, 32 heads on 8) take 1090 us, 1040 TFLOP/s (1284 us in a long
+// run at the clock that the power limit leaves): a tile's softmax waits for
+// its S, which waits for its last product with V, and only two tiles fit into
+// TMEM to fill the gap.  Selected keys, 64 rows of the 128: 1.7 us a tile in
+// bf16 and 2.2 in e4m3, the two streams' round trips, not a unit (without the
+// copies 1.75, without the conversions 2.1; warps whose lanes hold no row
+// leaving the softmax out gained nothing), and 7 to 11 us an item to fill the
+// pipeline.
 #include "attend.h"
 
 namespace pivot {

@@ -4,8 +4,11 @@
 // The state (table, lengths, reference counts) is kept on the device by
 // integer operations whose result does not depend on their order, so equal
 // calls leave equal states.  All of it is bound by memory: the bookkeeping
-// by latency (a few kilobytes, so as few launches and passes as possible),
-// the copies by bandwidth.
+// by latency (a few kilobytes, so as few launches and passes as possible: one
+// block plans, a second kernel moves), the copies by bandwidth.  Measured, at
+// 6.54 TB/s for a plain copy: an append of 17K bf16 tokens with shared pages
+// 41 us (155 MB, 24 us at that rate), a compaction that moves half of a large
+// pool 232 us (1.25 GB, 192 us).
 #include "pages.h"
 
 namespace pivot {
@@ -333,7 +336,9 @@ __global__ void __launch_bounds__(256)
     const int pieces = (int)((bytes + PIECE - 1) / PIECE);
     const long long jobs = (long long)n * pieces;
     // the same piece of every page, then the next: copies of one source read
-    // it from L2 together (48 copies of 16 rows of 8 MB: 95 -> 83 us)
+    // it from L2 together (48 branches of 16 caches with 4 MB of indexer keys
+    // each, fork and copy: 137 -> 101 us, 64 bytes a thread in flight
+    // included; the floor is 74)
     for (long long j = blockIdx.x; j < jobs; j += gridDim.x) {
         const int i = (int)(j % n);
         const int a = src_ids[i], b = dst_ids[i];

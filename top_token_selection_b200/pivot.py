@@ -736,8 +736,9 @@ def decode_attention(batch: PivotDecode, cache: PivotCache, q, k_new, v_new, mod
     names each token's positions, and attention (q bf16 [B, Gm, Hq, D])
     reads them.  batch.cache_len counts the new tokens: the lengths that the
     append leaves (it may be the cache's own length tensor).  Returns
-    (o [B, Gm, Hq, D], lse or None, idx, lack); a lack above 0 (on the
-    device) says that the pages ran out and o is not to be used."""
+    (o [B, Gm, Hq, D], lse or None, idx, lack); a lack other than 0 (on the
+    device) says that nothing was appended: o and idx are then not to be used,
+    and the error word may be set (a sequence shorter than Gm)."""
     B, Gm = batch.B, batch.Gm
     dev = cache.device
     if cache.B != B or tuple(q.shape[:2]) != (B, Gm):
