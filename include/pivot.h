@@ -354,10 +354,12 @@ pivot_status_t pivot_decode_noalloc(const pivot_decode_t* batch, int32_t mode, i
  * What the host cannot check sets the error word (PIVOT_ERR_DEVICE).  Row
  * offsets, sequence ids, counts or lengths out of range: the append and the
  * page calls then change nothing, and attention leaves the rows of that
- * sequence unwritten.  A page id out of range: the append changes nothing,
- * the other page calls pass over that table entry, and attention counts the
- * page's tokens as masked (selected: rows whose own token lies on it may stay
- * unwritten). */
+ * sequence unwritten.  Row offsets that descend: paged attention leaves every
+ * row unwritten (selected attention looks a row's sequence up and may find
+ * another that claims it).  A page id out of range: the append changes
+ * nothing, the other page calls pass over that table entry, and attention
+ * counts the page's tokens as masked (selected: rows whose own token lies on
+ * it may stay unwritten). */
 typedef struct {
     int32_t dtype;               /* PIVOT_BF16 or PIVOT_E4M3                     */
     int32_t B, Hkv, D;           /* sequences, key/value heads, head dim         */

@@ -17,19 +17,24 @@ namespace {
 constexpr int PLAN_THREADS = 1024;
 
 // One block.  Per sequence the row blocks, per row block the key tiles;
-// running sums of both.
+// running sums of both.  Offsets that never descend give the sequences rows
+// of their own, total at most, and blk_units has room for their blocks;
+// sequences between offsets that descend somewhere could claim the same rows
+// again and again, so such a call has no units at all.
 __global__ void __launch_bounds__(PLAN_THREADS) attend_plan_kernel(const AttendParams p) {
     __shared__ int tmp[33];
     const int B = p.c.B;
     let_next_start();
     // row blocks before each sequence
     int carry = 0;
+    bool descends = false;
     for (int b0 = 0; b0 < B; b0 += PLAN_THREADS) {
         const int b = b0 + threadIdx.x;
         int nb = 0;
         if (b < B) {
             int first, n, len;
             bool ok = new_rows(p.c, p.cu, b, p.total, p.max_new, first, n, len);
+            descends = descends || p.cu[b + 1] < p.cu[b];
             if (ok && len < n) {
                 raise_error(ERRBIT_DATA);
                 ok = false;
@@ -42,7 +47,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) attend_plan_kernel(const AttendP
         carry += tot;
     }
     if (threadIdx.x == 0) p.blk_off[B] = carry;
-    __syncthreads();
+    if (__syncthreads_or(descends)) {          // new_rows has set the error word
+        if (threadIdx.x == 0) p.seq_units[B] = 0;
+        return;
+    }
     // tiles of every row block: running sums over the call's blocks first
     const int nblk = carry;
     long long run = 0;
