@@ -451,9 +451,15 @@ size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
  * products as f16.  With up to 32 query rows a key they go in exactly and
  * their scales stay in fp32; with more, a key's scale is split into 7 bits that
  * go in with the code, exactly, and a rest in fp32, and a value's scale and
- * its product with the code are rounded to f16 (2^-12 each).  A value whose
- * scale is below 2^-14 of the largest of its tile of 32 to 128 tokens loses
- * bits, and so does, with more than 32 rows, such a key. */
+ * its product with the code are rounded to f16 (2^-12 each).  There a scale
+ * below 2^-21 of the largest of its tile of 128 tokens, or below 2^-90, loses
+ * bits.
+ * An f16 weight, times the scale of its value (more than 32 rows: the largest
+ * of the tile), keeps 11 bits down to 2^-24 (2^-15) of the largest of them so
+ * far, and an error of 2^-35 (2^-26) of it below.  Tokens without values take
+ * no part in that comparison up to 2^70 times the others' weights (more than
+ * 32 rows: if their scale is 1, as an append stores it), so a token of zeros
+ * may hold nearly all of the weight. */
 typedef struct {
     int32_t Hq;                  /* query heads, a multiple of Hkv               */
     int32_t total;               /* rows of q                                    */

@@ -1,0 +1,86 @@
+"""Attention over the paged cache where the size of a value, a scale or a score
+is out of the ordinary: on both kernels, against 64 bits."""
+import pytest
+import torch
+
+from test_gpu_cache import DEV, Cache, agree, expected, fill, i32, offsets
+from top_token_selection_b200 import pivot as pv
+
+pytestmark = pytest.mark.gpu
+
+# sequences (over the same pages, with the same queries), new tokens, query
+# heads (of one key head), selected positions (0: paged): the rows kernel with
+# 16 and 32 rows a key, then the tensor-memory kernel with blocks of 128 rows,
+# of 256 and selected.  One sequence's tiles are spread over all SMs; of many
+# sequences one block runs whole rows.
+FORMS = [(1, 1, 4, 0), (300, 1, 4, 0), (1, 3, 10, 0), (300, 3, 10, 0), (300, 1, 4, 1), (1, 2, 4, 1),
+         (1, 40, 2, 0), (150, 40, 2, 0), (1, 70, 8, 0), (150, 100, 2, 0), (1, 2, 40, 1), (150, 1, 40, 1)]
+
+
+def attend(c, q, B, length, picked, scale=None):
+    """The call's result and what it is in 64 bits, for B sequences alike."""
+    n, idx = q.shape[0], None
+    table = c.table.repeat(B, 1)
+    many = pv.make_cache(c.k, c.v, table, c.len.repeat(B), c.refs, c.ks, c.vs)
+    qs = q.repeat(B, 1, 1)
+    if picked is None:
+        got = pv.paged_attention(many, qs, offsets([n] * B), n, scale=scale, with_lse=True)
+    else:
+        idx = picked.to(torch.int32).to(DEV).repeat(n, 1).contiguous()
+        got = pv.selected_attention(many, qs, offsets([n] * B), n, idx.repeat(B, 1), scale=scale, with_lse=True)
+    torch.cuda.synchronize()
+    want = expected(c, q, [n], [length], idx=idx, scale=scale)
+    return got, tuple(x.repeat(B, *[1] * (x.dim() - 1)) for x in want)
+
+
+# A token without values that holds most of the weight, as an attention sink
+# or a padded token does: the append stores scale 1 for it.  The others' sum is
+# held to the same part of sum p |v| as ever (its own |v| is 0).
+@pytest.mark.parametrize("B,n,Hq,topk", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("length,empty,zero_key,size", [
+    (3000, [0], False, 1.0), (3000, [0], True, 0.1), (3000, [1500], False, 1e-3),
+    (2600, list(range(300)), True, 1e-2), (900, [0, 5, 899 - 80], False, 1e-4), (30000, [0], False, 1.0)])
+def test_a_heavy_token_without_values(D, B, n, Hq, topk, length, empty, zero_key, size):
+    gen = torch.Generator().manual_seed(length + D)
+    c = Cache(1, -(-length // 64), -(-length // 64), 64, 1, D, True)
+    u = torch.randn(D, generator=gen)
+    u /= u.norm()
+    k = torch.randn(length, 1, D, generator=gen)
+    v = torch.randn(length, 1, D, generator=gen) * size
+    # the empty tokens' scores lie `lift` above the others', so that each holds
+    # about 0.9 / len(empty) of the weight
+    lift = float(torch.tensor(10.0 * length / len(empty)).log()) * D ** 0.5 / 8
+    q = (8 * u + 0.3 * torch.randn(n, Hq, D, generator=gen)).to(torch.bfloat16).to(DEV)
+    along = (k @ u)[..., None] * u
+    k = k - along + 0.02 * along / D ** 0.5
+    if zero_key:
+        k = k - lift * u
+    k[empty] = 0.0 if zero_key else lift * u
+    v[empty] = 0.0
+    k, v = (x.to(torch.bfloat16).to(DEV) for x in (k, v))
+    assert int(pv.cache_append(c.c, k, v, i32([0, length]), length)) == 0
+    assert float(c.vs[c.table[0, empty[0] // 64], empty[0] % 64]) == 1.0
+    picked = torch.randperm(length - n, generator=gen)[: length * 3 // 4] if topk else None
+    if topk:
+        picked = torch.unique(torch.cat([picked, torch.tensor(empty)]))
+        picked = picked[torch.randperm(len(picked), generator=gen)]
+    got, want = attend(c, q, B, length, picked)
+    # most of the weight is the empty tokens': the others' sum is small
+    assert float((want[2].mean() / (v.float().abs().mean()))) < 0.4
+    agree(got, want)
+
+
+@pytest.mark.parametrize("B,n,Hq,topk", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_very_different_tokens(D, B, n, Hq, topk):
+    # one token's values are 2^10 of the others', and its weight small: neither
+    # takes bits from the other
+    gen = torch.Generator().manual_seed(20)
+    c, _ = fill([4000], 32, 1, D, True, seed=20)
+    page, slot = int(c.table[0, 60]), 7
+    c.vs[page, slot] *= 1024.0
+    c.ks[page, slot] *= 2.0 ** -6
+    q = torch.randn(n, Hq, D, generator=gen).to(torch.bfloat16).to(DEV)
+    picked = torch.randperm(4000 - n, generator=gen)[:3000] if topk else None
+    agree(*attend(c, q, B, 4000, picked))

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                 ring_ok[S::STAGES - 2] = put_ok;
             }
             const uint32_t kbase = my_ring + stage * S::STAGE, vbase = kbase + S::HALF;
-            const float* sc = my_scales + stage * 2 * KW;
+            float* sc = my_scales + stage * 2 * KW;
             if (++stage == S::STAGES) stage = 0;
             const uint32_t every = KW == 32 ? 0xffffffffu : 0xffffu;
             if ((ok & every) == 0) continue;                   // nothing in this step counts
@@ -488,31 +488,67 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                         s[mt][n][e] = x;
                     }
 
-            // ---- running maximum (e4m3: of weight times value scale, see
-            // log2_above); the sums move only when it grew
+            // ---- reference point: the running maximum (e4m3: see E4M3_HEAD);
+            // the sums move only when it does
             float lv = 0.0f;
-            if constexpr (FP8) lv = log2_above(sc[KW + lane]);
+            if constexpr (FP8) lv = log2_above<LOG2_V>(sc[KW + lane]);
             uint32_t pf[MT][NT / 2][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                float mx[2] = {-INFINITY, -INFINITY};
+                float mx[2];
+                auto largest = [&](uint32_t keys) {
+                    mx[0] = mx[1] = -INFINITY;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mx[0] = fmaxf(mx[0], fmaxf(s[mt][n][0], s[mt][n][1]));
-                    mx[1] = fmaxf(mx[1], fmaxf(s[mt][n][2], s[mt][n][3]));
-                }
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                    if constexpr (FP8) mx[e] += lv;
-                    mx[e] = fmaxf(mx[e], m[mt][e]);
-                }
-                if (__any_sync(0xffffffffu, mx[0] != m[mt][0] || mx[1] != m[mt][1])) {
+                        for (int e = 0; e < 4; ++e)
+                            if (!FP8 || ((keys >> (n * 8 + c4 * 2 + (e & 1))) & 1))
+                                mx[e >> 1] = fmaxf(mx[e >> 1], s[mt][n][e]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float f = m[mt][e] == -INFINITY ? 0.0f : ex2(m[mt][e] - mx[e]);
-                        m[mt][e] = mx[e];
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                    }
+                };
+                largest(0xffffffffu);
+                bool move = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (FP8)
+                        move = move || mx[e] + lv - m[mt][e] > E4M3_LAG;
+                    else
+                        move = move || mx[e] > m[mt][e];
+                }
+                if (__any_sync(0xffffffffu, move)) {
+                    if constexpr (FP8) {
+                        // which keys have values: a lane looks at one, as far as it has to
+                        uint32_t some = 0;
+#pragma unroll 1
+                        for (int ch = 0; ch < S::CH && !__all_sync(0xffffffffu, some & 0x7F7F7F7Fu); ++ch) {
+                            uint32_t x, y, z, w;
+                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+                                         : "r"(vbase + key_chunk<S::ROWB>(lane, ch)));
+                            some |= x | y | z | w;
+                        }
+                        const bool has = (some & 0x7F7F7F7Fu) != 0;
+                        const uint32_t keys = __ballot_sync(0xffffffffu, has);
+                        const float all[2] = {mx[0], mx[1]};
+                        if (keys != 0xffffffffu) {
+                            if (!has) sc[KW + lane] = 0.0f;
+                            __syncwarp();
+                            lv = log2_above<LOG2_V>(sc[KW + lane]);
+                            largest(keys);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e] + lv, all[e] - EMPTY_BELOW);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (FP8 && !(mx[e] - m[mt][e] > E4M3_LAG)) continue;
+                        const float to = FP8 ? point_at(m[mt][e], mx[e], E4M3_HEAD) : fmaxf(mx[e], m[mt][e]);
+                        const float f = m[mt][e] == -INFINITY ? 0.0f : ex2(m[mt][e] - to);
+                        m[mt][e] = to;
                         l[mt][e] *= f;
 #pragma unroll
                         for (int n = 0; n < D / 8; ++n) {
@@ -521,8 +557,8 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                         }
                     }
                 }
-                const float z0 = mx[0] == -INFINITY ? 0.0f : mx[0];
-                const float z1 = mx[1] == -INFINITY ? 0.0f : mx[1];
+                const float z0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0];
+                const float z1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float e0 = ex2(s[mt][n][0] - z0), e1 = ex2(s[mt][n][1] - z0);

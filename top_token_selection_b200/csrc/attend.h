@@ -158,17 +158,33 @@ __device__ __forceinline__ Item find_item(const AttendParams& p, long long u) {
     return it;
 }
 
-// For the value scales of a warp's 32 keys: the log2 of the power of two at
-// or above their largest size, within [-100, 100] (0 if all are 0).  The
-// reference point of an e4m3 softmax is raised by it, so that weight times
-// scale is at most 1 (f16 keeps 11 bits of it down to 2^-14 and an absolute
-// 2^-25 below), and l and o stay in the same units.
+// The reference point m of an e4m3 softmax stands over weight times value
+// scale, so that their product fits f16 whatever the scales.  m moves when one
+// could pass 2^E4M3_LAG (f16 ends below 2^16); a move puts the largest at about
+// 2^E4M3_HEAD (the rows kernel; the tensor-memory kernel, where a move costs
+// more, at 2).  11 bits are kept down to 2^-14 and an absolute 2^-25 below:
+// down to 2^-24 (2^-15) of the largest, and 2^-35 (2^-26) of it.  l and o are
+// in the same units.  Keys without values do not raise m, whatever their
+// scale: they add to l only, and m follows them at a distance of
+// 2^EMPTY_BELOW, where l (up to 2^26 such keys) still fits fp32.
+constexpr float E4M3_HEAD = 10.0f, E4M3_LAG = 15.0f, EMPTY_BELOW = 70.0f;
+// Beside a larger m fp32 holds no such distances: the largest is then put at 1.
+constexpr float HUGE_POINT = 1048576.0f;
+
+// Where m goes for a largest of `top` (it moves if top - m > E4M3_LAG).
+__device__ __forceinline__ float point_at(float m, float top, float head) {
+    return fmaxf(m, fabsf(top) > HUGE_POINT ? top : top - head);
+}
+
+// For scales of a warp's 32 keys: the log2 of the power of two at or above
+// their largest size, within [LO, 100] (LO if all are 0).
+template <int LO>
 __device__ __forceinline__ float log2_above(float scale) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(scale)));
-    if (top == 0) return 0.0f;
     const int e = (int)((top + 0x007FFFFFu) >> 23) - 127;
-    return (float)(e < -100 ? -100 : e > 100 ? 100 : e);
+    return (float)(e < LO ? LO : e > 100 ? 100 : e);
 }
+constexpr int LOG2_K = -100, LOG2_V = -70;    // the lowest for scales of K and of V (-EMPTY_BELOW)
 
 // One thread of each CTA: the record of the item that holds the first unit of
 // its run, if an earlier CTA began it and no other CTA's run begins between.

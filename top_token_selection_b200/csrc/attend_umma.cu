@@ -66,6 +66,13 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// The same of weights that may pass the type's range: those of keys without
+// values, which meet zeros.
+__device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
@@ -134,6 +141,11 @@ __device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b)
 __device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& a, uint32_t& b) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -167,8 +179,8 @@ __device__ __forceinline__ void weights(const float* s, float c, float z, const 
             e[y + 1] = ex2(e[y + 1]);
             sum[y / 2] = add2(sum[y / 2], pack2(e[y], e[y + 1]));
         }
-        pk[k / 2] = FP8 ? f16x2(e[0], e[1]) : bf16x2(e[0], e[1]);
-        pk[k / 2 + 1] = FP8 ? f16x2(e[2], e[3]) : bf16x2(e[2], e[3]);
+        pk[k / 2] = FP8 ? f16x2_sat(e[0], e[1]) : bf16x2(e[0], e[1]);
+        pk[k / 2 + 1] = FP8 ? f16x2_sat(e[2], e[3]) : bf16x2(e[2], e[3]);
     }
     tmem_st16(to, pk);
 }
@@ -209,7 +221,9 @@ struct UmmaShape {
     // they are converted into the ring
     static constexpr int CSTAGES = 3;
     static constexpr int STAGING = FP8 ? CSTAGES * TKEYS * D : 0;
-    // per tile: which keys count, and for e4m3 their scales; selected: rows
+    // per tile: which keys count, and for e4m3 their scales; selected: rows.
+    // (A load of m_empty, or of the scales, where m moves instead of at the
+    // tile's beginning: mixed chunks 218 -> 228 us.)
     static constexpr int MS = 8;
     static constexpr int META = MS * (16 + (FP8 ? 16 + TKEYS * 12 : 0) + (SELECTED ? TKEYS * 4 : 0));
     static constexpr int SMEM = 1024 + QTILES * TILE + STAGES * TILE + STAGING + META + 1024 + 512 + 2 * 48 + TKEYS;
@@ -229,7 +243,9 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     using S = UmmaShape<D, FP8, SELECTED, SPLIT>;
     constexpr int STAGES = S::STAGES, MS = S::MS;
     constexpr int R = SPLIT ? 128 : 256;
-    constexpr float LAG = FP8 ? 14.0f : 64.0f, FAR = FP8 ? 512.0f : 1048576.0f;
+    constexpr float LAG = FP8 ? E4M3_LAG : 64.0f, HEAD = FP8 ? 1.0f : 0.0f;
+    constexpr float FAR = FP8 ? 512.0f : HUGE_POINT;
+    constexpr float UP = 7.0f;                            // e4m3: see the tiles' scales
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -240,6 +256,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     uint32_t* m_ok = reinterpret_cast<uint32_t*>(sM);     // [MS][4]
     float* m_lv = reinterpret_cast<float*>(sM + MS * 16); // [MS] log2_above of the scales of V
     float* m_lk = m_lv + MS;                              // [MS] and of K
+    float* m_empty = m_lk + MS;                           // [MS] not 0: some key has no scale of V
     float* m_ks = m_lv + MS * 4;                          // [MS][128] scales over those
     float* m_rest = m_ks + MS * TKEYS;                    // [MS][128] what m_ks leaves of a key's scale
     float* m_vs = m_rest + MS * TKEYS;
@@ -458,16 +475,37 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                         make_int4(row[0] >= 0 ? row[0] : spare, row[1] >= 0 ? row[1] : spare,
                                   row[2] >= 0 ? row[2] : spare, row[3] >= 0 ? row[3] : spare);
                 if constexpr (FP8) {
+                    // a token without values (its scale is 1, as an append
+                    // stores it): no scale, so that it takes no bits from the
+                    // tile's values and the softmax knows it
+                    float empty = 0.0f;
+                    if (__any_sync(0xffffffffu, vs[0] == 1.0f || vs[1] == 1.0f || vs[2] == 1.0f || vs[3] == 1.0f)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                            for (uint32_t ones = __ballot_sync(0xffffffffu, vs[i] == 1.0f); ones; ones &= ones - 1) {
+                                const int of = __ffs(ones) - 1;    // all lanes look at this one's key
+                                const size_t at = (size_t)__shfl_sync(0xffffffffu, row[i], of) * p.c.rowb + it.h * D;
+                                const uint32_t codes =
+                                    lane < D / 4 ? __ldg(reinterpret_cast<const uint32_t*>(p.c.v + at) + lane) : 0;
+                                if (!__any_sync(0xffffffffu, codes & 0x7F7F7F7Fu)) {
+                                    if (lane == of) vs[i] = 0.0f;
+                                    empty = 1.0f;
+                                }
+                            }
+                    }
                     // scales relative to the power of two at or above the
-                    // tile's largest
-                    const float lk = log2_above(fmaxf(fmaxf(fabsf(ks[0]), fabsf(ks[1])),
-                                                      fmaxf(fabsf(ks[2]), fabsf(ks[3]))));
-                    const float lv = log2_above(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
-                                                      fmaxf(fabsf(vs[2]), fabsf(vs[3]))));
-                    const float dk = exp2_whole(-lk), dv = exp2_whole(-lv);
+                    // tile's largest, times 2^UP: codes of up to 448 then
+                    // use f16 from its top
+                    const float lk = log2_above<LOG2_K>(fmaxf(fmaxf(fabsf(ks[0]), fabsf(ks[1])),
+                                                              fmaxf(fabsf(ks[2]), fabsf(ks[3]))));
+                    const float lv = log2_above<LOG2_V>(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
+                                                              fmaxf(fabsf(vs[2]), fabsf(vs[3]))));
+                    const float dk = exp2_whole(UP - lk), dv = exp2_whole(UP - lv);
                     if (lane == 0) {
-                        m_lk[ms] = lk;
+                        m_lk[ms] = lk - UP;
                         m_lv[ms] = lv;
+                        m_empty[ms] = empty;
                     }
                     // a key's scale in two factors: 7 bits that go into its
                     // halves, exactly (a code has 4), and the rest, within
@@ -905,6 +943,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                 sph ^= 1;
                 // e4m3: factor of the tile's scores, and log2 of its values'
                 const float ct = FP8 ? c * exp2_whole(m_lk[ms]) : c, lv = FP8 ? m_lv[ms] : 0.0f;
+                const bool empty = FP8 && m_empty[ms] != 0.0f;
                 const uint2 ok = *reinterpret_cast<const uint2*>(m_ok + ms * 4 + 2 * x);
                 const int key0 = (ta + j) * TKEYS + 64 * x;
                 const bool plain = (ok.x & ok.y) == 0xffffffffu &&
@@ -934,14 +973,14 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
 #pragma unroll
                         for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[k + y], s[k + 4 + y]);
                 };
-                // The reference point may lag behind the maximum by LAG:
-                // weights then reach 2^LAG, which costs no precision (bf16 has
-                // the exponents of fp32; f16 ends at 2^16), and m and the sums
-                // in TMEM seldom have to move (2048 new tokens over 32K, bf16:
-                // 1147 us with a lag of 8, 1088 with 64).  For e4m3 m stands
-                // over the weights times the values' scales, so that their
-                // product fits f16 whatever the scales; the sums of both are
-                // in its units, which cancel in o.
+                // The reference point m may lag behind the maximum, so that m
+                // and the sums in TMEM seldom have to move (2048 new tokens
+                // over 32K, bf16: 1147 us with weights of up to 2^8, 1088 with
+                // 2^64): bf16 has the exponents of fp32.  For f16 weights see
+                // E4M3_LAG: m stands over weight times the tile's lv, and a
+                // move puts the largest at 2^HEAD = 2, not higher (2^10: 295
+                // -> 375 us for chunks over 2048 selected keys, for m moves
+                // five times as often).
                 float top = -INFINITY;
                 if (!aborted) {
                     float a[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -958,21 +997,28 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     if (FP8 && top > -INFINITY) top += fabsf(top - lv) * 0.0078125f;
                 }
                 const float* rest = m_rest + ms * TKEYS + 64 * x;
-                if (group_any<64>(pair, top > m + LAG)) {
+                if (group_any<64>(pair, top - m > LAG)) {
                     if constexpr (FP8) {
-                        if (__any_sync(0xffffffffu, fabsf(top) > FAR && top > -INFINITY) && !aborted) {
-                            top = -INFINITY;               // with the rest of the scales
+                        const float* vs = m_vs + ms * TKEYS + 64 * x;
+                        if (__any_sync(0xffffffffu, empty || (fabsf(top) > FAR && top > -INFINITY)) && !aborted) {
+                            // with the rest of the scales; keys without values
+                            // (scale 0) EMPTY_BELOW below what l or, lv > 0,
+                            // their weight here takes
+                            const float below = EMPTY_BELOW + fminf(lv, 0.0f);
+                            top = -INFINITY;
 #pragma unroll 1
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t b[16];
-                                tmem_ld16(tS + 64 * x + 16 * i, b);
+                            for (int i = 0; i < 8; ++i) {
+                                uint32_t b[8];
+                                tmem_ld8(tS + 64 * x + 8 * i, b);
                                 tmem_ld_wait();
-                                const uint32_t see = seen(i >> 1) >> (16 * (i & 1));
+                                const uint32_t see = seen(i >> 2) >> (8 * (i & 3));
 #pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if ((see >> k) & 1)
-                                        top = fmaxf(top, __fadd_rn(__fmul_rn(__uint_as_float(b[k]),
-                                                                             __fmul_rn(ct, rest[16 * i + k])), lv));
+                                for (int k = 0; k < 8; ++k)
+                                    if ((see >> k) & 1) {
+                                        const float a = __fadd_rn(
+                                            __fmul_rn(__uint_as_float(b[k]), __fmul_rn(ct, rest[8 * i + k])), lv);
+                                        top = fmaxf(top, vs[8 * i + k] != 0.0f ? a : a - below);
+                                    }
                             }
                         }
                     }
@@ -980,9 +1026,10 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     named_bar_sync(pair, 64);
                     top = key_to_float(m_top[t * 128 + r]);
                     float f = 1.0f;
-                    if (top > m + LAG) {
-                        f = m == -INFINITY ? 0.0f : ex2(m - top);
-                        m = top;
+                    if (top - m > LAG) {
+                        const float to = point_at(m, top, HEAD);
+                        f = m == -INFINITY ? 0.0f : ex2(m - to);
+                        m = to;
                     }
                     l *= f;
                     far = __any_sync(0xffffffffu, fabsf(m) > FAR && m > -INFINITY);
@@ -1112,8 +1159,8 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                 constexpr int PARTS = SPLIT ? D / 64 : D / 32;     // 16 values each
                 const int first = (SPLIT ? 2 * t + x : x) * PARTS;
                 float* part = p.part + (size_t)slot * slot_words(R, D);
-                f0 *= inv;
-                f1 *= inv;
+                f0 *= FP8 ? inv * exp2_whole(-UP) : inv;
+                f1 *= FP8 ? inv * exp2_whole(-UP) : inv;
 #pragma unroll
                 for (int i = first; i < first + PARTS; ++i) {
                     float o[16];
