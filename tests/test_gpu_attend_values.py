@@ -84,3 +84,21 @@ def test_values_of_very_different_tokens(D, B, n, Hq, topk):
     q = torch.randn(n, Hq, D, generator=gen).to(torch.bfloat16).to(DEV)
     picked = torch.randperm(4000 - n, generator=gen)[:3000] if topk else None
     agree(*attend(c, q, B, 4000, picked))
+
+
+# Scores that are all (nearly) 0: a mean of the values.
+@pytest.mark.parametrize("B,n,Hq,topk", FORMS)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("what", ["queries", "keys", "scale", "all"])
+def test_scores_of_nothing_beside_masked_keys(what, fp8, B, n, Hq, topk):
+    c, gen = fill([700], 16, 1, 128, fp8, seed=21)
+    q = torch.randn(n, Hq, 128, generator=gen).to(torch.bfloat16).to(DEV)
+    if what in ("queries", "all"):
+        q[:, 1::2] = 0.0
+        q[0] = 0.0
+    if fp8 and what in ("keys", "all"):
+        c.ks *= 2.0 ** -30
+    picked = None
+    if topk:
+        picked = torch.cat([torch.arange(300), torch.full((50,), -1), torch.tensor([699, 2 ** 31 - 1])])
+    agree(*attend(c, q, B, 700, picked, scale={"scale": 1e-8, "all": 1e-30}.get(what)))

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                 const uint32_t e =
                     min(max(__float_as_uint(amax) & 0x7F800000u, 0x01000000u), 0x7D800000u);
                 const float down = __uint_as_float(0x7F000000u - e);
-                mul *= __uint_as_float(e);
+                mul = fminf(mul * __uint_as_float(e), 0x1p127f);   // a score of 0 stays 0
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
                     x[i] = f16x2(__uint_as_float(x[i] << 16) * down,

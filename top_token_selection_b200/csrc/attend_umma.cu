@@ -941,8 +941,11 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     if (!__all_sync(0xffffffffu, got)) aborted = true;
                 }
                 sph ^= 1;
-                // e4m3: factor of the tile's scores, and log2 of its values'
-                const float ct = FP8 ? c * exp2_whole(m_lk[ms]) : c, lv = FP8 ? m_lv[ms] : 0.0f;
+                // e4m3: factor of the tile's scores, and log2 of its values'.
+                // Scores are below 2^32 here: a smaller factor is as good as
+                // 2^-120, and 0 would make NaN of the masked ones' -inf.
+                const float ct = FP8 ? fminf(fmaxf(c * exp2_whole(m_lk[ms]), 0x1p-120f), 0x1p120f) : c,
+                            lv = FP8 ? m_lv[ms] : 0.0f;
                 const bool empty = FP8 && m_empty[ms] != 0.0f;
                 const uint2 ok = *reinterpret_cast<const uint2*>(m_ok + ms * 4 + 2 * x);
                 const int key0 = (ta + j) * TKEYS + 64 * x;
