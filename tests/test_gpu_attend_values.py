@@ -102,3 +102,24 @@ def test_scores_of_nothing_beside_masked_keys(what, fp8, B, n, Hq, topk):
     if topk:
         picked = torch.cat([torch.arange(300), torch.full((50,), -1), torch.tensor([699, 2 ** 31 - 1])])
     agree(*attend(c, q, B, 700, picked, scale={"scale": 1e-8, "all": 1e-30}.get(what)))
+
+
+@pytest.mark.parametrize("B,n,Hq,topk", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [20, -20, 60])
+def test_large_scores_beside_large_value_scales(power, D, B, n, Hq, topk):
+    # scores of 1e28 choose one key: the output is its values, to the bf16
+    # rounding of o (2^-9) and one of a weight of 1 in f16 with the scale's (2^-11 twice)
+    c, gen = fill([400], 32, 1, D, True, seed=22)
+    q = torch.randn(n, Hq, D, generator=gen)
+    q[:, 1::2] *= 1e28
+    q = q.to(torch.bfloat16).to(DEV)
+    c.vs *= 2.0 ** power
+    picked = torch.randperm(400 - n, generator=gen)[:300] if topk else None
+    got, want = attend(c, q, B, 400, picked)
+    assert pv.device_error() == 0
+    assert bool(torch.isfinite(got[0].float()).all()) and bool(torch.isfinite(got[1]).all())
+    big = (got[0].double() - want[0]).abs()[:, 1::2] / want[2][:, 1::2]
+    assert float(big.max()) < 2 ** -8 + 2 ** -10
+    assert float((got[1].double() / want[1] - 1).abs()[:, 1::2].max()) < 2 ** -16
+    agree(tuple(x[:, ::2] for x in got), tuple(x[:, ::2] for x in want))

@@ -297,8 +297,10 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
         const int key_lo = p.window ? max(0, lim_lo - p.window + 1) : 0;   // first position any row reads
 
         float m[MT][2], l[MT][2], acc[MT][D / 8][4];
+        bool huge[MT];           // |m| > HUGE_POINT in some row of the warp
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
+            huge[mt] = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) { m[mt][e] = -INFINITY; l[mt][e] = 0.0f; }
 #pragma unroll
@@ -556,9 +558,22 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                             acc[mt][n][2 * e + 1] *= f;
                         }
                     }
+                    if constexpr (FP8)
+                        huge[mt] = __any_sync(0xffffffffu, (fabsf(m[mt][0]) > HUGE_POINT && m[mt][0] > -INFINITY) ||
+                                                               (fabsf(m[mt][1]) > HUGE_POINT && m[mt][1] > -INFINITY));
                 }
-                const float z0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0];
-                const float z1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
+                float z0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0];
+                float z1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
+                if (FP8 && huge[mt]) {
+                    // fp32 loses the scale in s + lv: scores are rounded as m
+                    // was, and their difference takes the scale out again
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[mt][n][e] = __fadd_rn(s[mt][n][e], lv) - (e < 2 ? z0 : z1) - lv;
+                    z0 = z1 = 0.0f;
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float e0 = ex2(s[mt][n][0] - z0), e1 = ex2(s[mt][n][1] - z0);
