@@ -123,3 +123,30 @@ def test_large_scores_beside_large_value_scales(power, D, B, n, Hq, topk):
     assert float(big.max()) < 2 ** -8 + 2 ** -10
     assert float((got[1].double() / want[1] - 1).abs()[:, 1::2].max()) < 2 ** -16
     agree(tuple(x[:, ::2] for x in got), tuple(x[:, ::2] for x in want))
+
+
+@pytest.mark.parametrize("B,n,Hq,topk", FORMS)
+@pytest.mark.parametrize("lift", [20.0, 43.5, 100.0])
+@pytest.mark.parametrize("size", [1e20, 1e34, 1e-30])
+def test_large_values_under_a_late_large_score(size, lift, B, n, Hq, topk):
+    # bf16 values far up and down the type's range; the keys at the end
+    # outweigh the first ones by e^lift
+    length, D = 1500, 64
+    c, gen = fill([length], 64, 1, D, False, seed=23)
+    u = torch.randn(D, generator=gen)
+    u /= u.norm()
+    q = (8 * u).repeat(n, Hq, 1).to(torch.bfloat16).to(DEV)
+    k = 0.05 * torch.randn(length, D, generator=gen)
+    k[1300:length - n] += lift * u
+    v = torch.randn(length, D, generator=gen) * size
+    t = torch.arange(length, device=DEV)
+    page, slot = c.table[0].long()[t // 64], t % 64
+    c.k[page, slot, 0], c.v[page, slot, 0] = k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV)
+    picked = torch.arange(length - n) if topk else None
+    got, want = attend(c, q, B, length, picked)
+    assert bool(torch.isfinite(got[0].float()).all())
+    # a score's fp32 error is up to D * 2^-24 of its size, 100: 2^-11; weights and
+    # outputs round to bf16, off by at most 2^-8 each
+    assert float(((got[0].double() - want[0]).abs() / want[2]).max()) < 2 * 2.0 ** -8 + 2.0 ** -10
+    assert float((got[1].double() - want[1]).abs().max()) < 5e-4
+    assert pv.device_error() == 0

@@ -243,7 +243,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
     using S = UmmaShape<D, FP8, SELECTED, SPLIT>;
     constexpr int STAGES = S::STAGES, MS = S::MS;
     constexpr int R = SPLIT ? 128 : 256;
-    constexpr float LAG = FP8 ? E4M3_LAG : 64.0f, HEAD = FP8 ? 1.0f : 0.0f;
+    constexpr float LAG = FP8 ? E4M3_LAG : 0.0f, HEAD = FP8 ? 1.0f : -24.0f;
     constexpr float FAR = FP8 ? 512.0f : HUGE_POINT;
     constexpr float UP = 7.0f;                            // e4m3: see the tiles' scales
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -976,14 +976,15 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
 #pragma unroll
                         for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[k + y], s[k + 4 + y]);
                 };
-                // The reference point m may lag behind the maximum, so that m
+                // The maximum may grow under the reference point m, so that m
                 // and the sums in TMEM seldom have to move (2048 new tokens
-                // over 32K, bf16: 1147 us with weights of up to 2^8, 1088 with
-                // 2^64): bf16 has the exponents of fp32.  For f16 weights see
-                // E4M3_LAG: m stands over weight times the tile's lv, and a
-                // move puts the largest at 2^HEAD = 2, not higher (2^10: 295
-                // -> 375 us for chunks over 2048 selected keys, for m moves
-                // five times as often).
+                // over 32K, bf16: 1147 us with room for 2^8, 1088 for 2^24 or
+                // 2^64).  bf16 weights have the exponents of fp32: a move puts
+                // the largest at 2^-24 and none passes 1, so sums of weight
+                // times value stay as small as the values.  For f16 weights
+                // see E4M3_LAG: m stands over weight times the tile's lv, and
+                // a move puts the largest at 2, not higher (2^10: 295 -> 375
+                // us for chunks over 2048 selected keys, for m moves more).
                 float top = -INFINITY;
                 if (!aborted) {
                     float a[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
