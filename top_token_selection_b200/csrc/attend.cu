@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attend_plan_kernel(const AttendP
         }
         int tot;
         const int x = block_exclusive(tiles, tmp, tot);
-        if (j < nblk) p.blk_units[j] = run + x + tiles;
+        if (j < nblk && PIVOT_CHECK(j < (long long)p.total * p.G / p.R + B)) p.blk_units[j] = run + x + tiles;
         run += tot;
     }
     __syncthreads();
@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
             if (page_a != -2) {
                 row = p.c.row_of(page_a, pos_a);
                 if (row < 0) raise_error(ERRBIT_DATA);
+                if (!PIVOT_CHECK(row < (long long)p.c.num_pages << p.c.page_log2)) row = -1;
             }
             put_ok = __ballot_sync(0xffffffffu, row >= 0);
             // the next step's page, the one after its positions
@@ -693,7 +694,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                 *reinterpret_cast<uint2*>(p.o + head * D + d) = y;
                 if (p.lse && d == 0)
                     p.lse[head] = none ? -INFINITY : (z + __log2f(sum)) * 0.6931471805599453f;
-            } else {
+            } else if (PIVOT_CHECK(slot < 2 * p.ncta)) {
                 float* to = p.part + (size_t)slot * slot_words(R, D);
                 *reinterpret_cast<float4*>(to + (size_t)r * D + d) = make_float4(o[0], o[1], o[2], o[3]);
                 if (d == 0) {
@@ -717,13 +718,10 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) 
     if (r >= j.rows) return;
     constexpr int PER = D / 32;
     const size_t words = slot_words(p.R, D);
-    // a CTA without units left nothing
-    auto there = [&](int i) { return i <= j.c1 && run_begin(j.units, i, j.ncta) < run_begin(j.units, i + 1, j.ncta); };
     auto sums = [&](int i) { return p.part + (size_t)(2 * i + (i == j.c0)) * words; };
     // a lane a partial: its maximum and sum
     float m = -INFINITY, l = 0.0f;
     for (int i = j.c0 + lane; i <= j.c1; i += 32) {
-        if (!there(i)) continue;
         const float* s = sums(i) + (size_t)p.R * D;
         const float mi = s[r], li = s[p.R + r];
         const float top = fmaxf(m, mi);
@@ -745,7 +743,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) 
         float x[4][PER], f[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            const bool ok = there(i0 + y);
+            const bool ok = i0 + y <= j.c1;
             const float* s = sums(ok ? i0 + y : j.c0);
             f[y] = ok ? ex2(s[(size_t)p.R * D + r] - z) : 0.0f;
 #pragma unroll

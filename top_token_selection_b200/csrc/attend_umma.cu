@@ -447,6 +447,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     if (counts(pos_a[i])) {
                         row[i] = p.c.row_of(page_a[i], pos_a[i]);
                         if (row[i] < 0) raise_error(ERRBIT_DATA);
+                        if (!PIVOT_CHECK(row[i] < (long long)p.c.num_pages << p.c.page_log2)) row[i] = -1;
                     }
                     ok |= (row[i] >= 0 ? 1u : 0u) << i;
                     pos_a[i] = pos_b[i];
@@ -1191,7 +1192,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                             y.w = bf16x2(o[8 * k + 6], o[8 * k + 7]);
                             *reinterpret_cast<uint4*>(p.o + head * D + i * 16 + k * 8) = y;
                         }
-                    } else if (live) {
+                    } else if (live && PIVOT_CHECK(slot < 2 * p.ncta)) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             *reinterpret_cast<float4*>(part + (size_t)rb * D + i * 16 + k * 4) =
@@ -1200,10 +1201,10 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     __syncwarp();
                 }
                 if (live && x == 0 && (!SPLIT || t == 0)) {
-                    if (!whole) {
+                    if (!whole && PIVOT_CHECK(slot < 2 * p.ncta)) {
                         part[(size_t)R * D + rb] = m;
                         part[(size_t)R * D + R + rb] = l;
-                    } else if (p.lse) {
+                    } else if (whole && p.lse) {
                         p.lse[head] = none ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
                     }
                 }

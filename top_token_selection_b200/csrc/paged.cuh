@@ -47,10 +47,6 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int B, int r) {
     return lo;
 }
 
-__device__ __forceinline__ int warp_sum(int v) {
-    return __reduce_add_sync(0xffffffffu, v);
-}
-
 // Exclusive prefix sum of one value per thread over a block of up to 1024
 // threads; `tot` receives the sum.  tmp: 33 ints of shared memory.
 __device__ __forceinline__ int block_exclusive(int v, int* tmp, int& tot) {

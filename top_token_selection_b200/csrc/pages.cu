@@ -29,8 +29,8 @@ struct AppendWs {
 
 // Ids of the lowest `want` free pages (refs 0), ascending, to list; returns
 // how many there are, up to want.  Whole block; each round reads 16 counts a
-// thread.
-__device__ int lowest_free(const int32_t* refs, int num_pages, int want, int32_t* list, int* tmp) {
+// thread.  room: entries of list.
+__device__ int lowest_free(const int32_t* refs, int num_pages, int want, int32_t* list, int room, int* tmp) {
     constexpr int PER = 16;
     int found = 0;
     for (int base = 0; base < num_pages && found < want; base += PLAN_THREADS * PER) {
@@ -57,7 +57,8 @@ __device__ int lowest_free(const int32_t* refs, int num_pages, int want, int32_t
         while (free_bits && rank < want) {
             const int i = __ffs(free_bits) - 1;
             free_bits &= free_bits - 1;
-            list[rank++] = at + i;
+            if (PIVOT_CHECK(rank < room)) list[rank] = at + i;
+            ++rank;
         }
         found += tot;
     }
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     }
     bad = __syncthreads_or(bad);
     int found = 0;
-    if (!bad) found = lowest_free(c.refs, c.num_pages, carry, w.list, tmp);
+    if (!bad) found = lowest_free(c.refs, c.num_pages, carry, w.list, total / P + 2 * c.B + 1, tmp);
     const bool fits = !bad && found == carry;
     if (threadIdx.x == 0) {
         w.head[0] = fits ? 1 : 0;
@@ -390,8 +391,8 @@ __global__ void __launch_bounds__(PLAN_THREADS)
         int a = moves + (x & 0xFFFF), b = holes + (x >> 16);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if ((of >> i) & 1) w.of[a++] = p0 + i;
-            if ((to >> i) & 1) w.to[b++] = p0 + i;
+            if (((of >> i) & 1) && PIVOT_CHECK(a <= c.num_pages / 2)) w.of[a++] = p0 + i;
+            if (((to >> i) & 1) && PIVOT_CHECK(b <= c.num_pages / 2)) w.to[b++] = p0 + i;
             if ((in >> i) & 1) w.remap[p0 + i] = (live >> i) & 1 ? p0 + i : -1;
         }
         moves += tot & 0xFFFF;
