@@ -83,27 +83,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) attend_plan_kernel(const AttendP
 }
 
 // ------------------------------------------------------- warp-level pieces
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// Two e4m3 codes as two halves (exact).
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
-    return r;
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -212,7 +191,14 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
     const uint32_t my_ring = smem_u32(ring) + warp * (S::STAGES * S::STAGE);
     float* my_scales = scales + warp * (S::STAGES * 2 * KW);
 
+    // e4m3: where some row's |m| passes HUGE_POINT, fp32 does not hold lv in it,
+    // and scales met f16 as they are.  The CTA then goes over the item again,
+    // each warp with its scales in units of 2^unit, the largest: its weights
+    // are larger by that, and m smaller.
+    bool again = false;
+    float unit = 0.0f;
     while (u < u_end) {
+        const long long u0 = u;
         const Item it = find_item<SELECTED>(p, u);
         const int ta = it.tile0 + (int)(u - it.unit0);
         const int tz = it.tile0 + (int)min((long long)it.tiles, u_end - it.unit0);
@@ -297,10 +283,8 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
         const int key_lo = p.window ? max(0, lim_lo - p.window + 1) : 0;   // first position any row reads
 
         float m[MT][2], l[MT][2], acc[MT][D / 8][4];
-        bool huge[MT];           // |m| > HUGE_POINT in some row of the warp
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            huge[mt] = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) { m[mt][e] = -INFINITY; l[mt][e] = 0.0f; }
 #pragma unroll
@@ -328,6 +312,16 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
             if (SELECTED && pos > it.pos0) return -2;
             return pos >= 0 ? ld_nc_early(pages + (pos >> p.c.page_log2)) : -2;
         };
+        if (FP8 && again) {
+            float most = 0.0f;
+#pragma unroll 1
+            for (int t = ta; t < tz; ++t) {
+                const int pos = position(t), page = page_of(pos);
+                const int row = page == -2 ? -1 : p.c.row_of(page, pos);
+                if (row >= 0) most = fmaxf(most, fabsf(p.c.vs[row]));
+            }
+            unit = log2_above<LOG2_LOW>(most);
+        }
         int pos_a = position(ta), page_a = page_of(pos_a);      // step to copy next
         int pos_b = position(ta + 1);                           // and the one after
         uint32_t ring_ok[S::STAGES];                            // keys that count, by stage
@@ -362,7 +356,8 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                 const uint32_t sd = smem_u32(my_scales + stage * 2 * KW) + kk * 4;
                 const int sr = row < 0 ? 0 : row;
                 cp4_or_zero(sd, p.c.ks + sr, row >= 0);
-                cp4_or_zero(sd + KW * 4, p.c.vs + sr, row >= 0);
+                if (unit == 0.0f) cp4_or_zero(sd + KW * 4, p.c.vs + sr, row >= 0);
+                else my_scales[stage * 2 * KW + KW + kk] = row >= 0 ? p.c.vs[sr] * exp2_whole(-unit) : 0.0f;
             }
         };
 #pragma unroll
@@ -491,40 +486,39 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                         s[mt][n][e] = x;
                     }
 
-            // ---- reference point: the running maximum (e4m3: see E4M3_HEAD);
-            // the sums move only when it does
+            // ---- reference point: the running maximum (e4m3: see E4M3_HEAD, lv
+            // is log2 of the step's largest value scale); the sums move only
+            // when it does
             float lv = 0.0f;
-            if constexpr (FP8) lv = log2_above<LOG2_V>(sc[KW + lane]);
+            if constexpr (FP8) {
+                lv = fmaxf(log2_above<LOG2_LOW>(sc[KW + lane]), -EMPTY_BELOW);
+            }
             uint32_t pf[MT][NT / 2][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                float mx[2];
-                auto largest = [&](uint32_t keys) {
-                    mx[0] = mx[1] = -INFINITY;
+                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    mx[0] = fmaxf(mx[0], fmaxf(s[mt][n][0], s[mt][n][1]));
+                    mx[1] = fmaxf(mx[1], fmaxf(s[mt][n][2], s[mt][n][3]));
+                }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!FP8 || ((keys >> (n * 8 + c4 * 2 + (e & 1))) & 1))
-                                mx[e >> 1] = fmaxf(mx[e >> 1], s[mt][n][e]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                    }
-                };
-                largest(0xffffffffu);
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                }
                 bool move = false;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if constexpr (FP8)
-                        move = move || mx[e] + lv - m[mt][e] > E4M3_LAG;
+                        move = move || (mx[e] + lv) - m[mt][e] > E4M3_LAG;
                     else
                         move = move || mx[e] > m[mt][e];
                 }
                 if (__any_sync(0xffffffffu, move)) {
                     if constexpr (FP8) {
-                        // which keys have values: a lane looks at one, as far as it has to
+                        // keys without values, whose scale does not count: a
+                        // lane looks at one, as far as it has to
                         uint32_t some = 0;
 #pragma unroll 1
                         for (int ch = 0; ch < S::CH && !__all_sync(0xffffffffu, some & 0x7F7F7F7Fu); ++ch) {
@@ -534,17 +528,13 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                                          : "r"(vbase + key_chunk<S::ROWB>(lane, ch)));
                             some |= x | y | z | w;
                         }
-                        const bool has = (some & 0x7F7F7F7Fu) != 0;
-                        const uint32_t keys = __ballot_sync(0xffffffffu, has);
-                        const float all[2] = {mx[0], mx[1]};
-                        if (keys != 0xffffffffu) {
-                            if (!has) sc[KW + lane] = 0.0f;
+                        if (!__all_sync(0xffffffffu, some & 0x7F7F7F7Fu)) {
+                            if (!(some & 0x7F7F7F7Fu)) sc[KW + lane] = 0.0f;
                             __syncwarp();
-                            lv = log2_above<LOG2_V>(sc[KW + lane]);
-                            largest(keys);
+                            lv = fmaxf(log2_above<LOG2_LOW>(sc[KW + lane]), -EMPTY_BELOW);
                         }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e] + lv, all[e] - EMPTY_BELOW);
+                        for (int e = 0; e < 2; ++e) mx[e] += lv;
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -559,22 +549,9 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                             acc[mt][n][2 * e + 1] *= f;
                         }
                     }
-                    if constexpr (FP8)
-                        huge[mt] = __any_sync(0xffffffffu, (fabsf(m[mt][0]) > HUGE_POINT && m[mt][0] > -INFINITY) ||
-                                                               (fabsf(m[mt][1]) > HUGE_POINT && m[mt][1] > -INFINITY));
                 }
-                float z0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0];
-                float z1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
-                if (FP8 && huge[mt]) {
-                    // fp32 loses the scale in s + lv: scores are rounded as m
-                    // was, and their difference takes the scale out again
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s[mt][n][e] = __fadd_rn(s[mt][n][e], lv) - (e < 2 ? z0 : z1) - lv;
-                    z0 = z1 = 0.0f;
-                }
+                const float z0 = m[mt][0] == -INFINITY ? 0.0f : m[mt][0];
+                const float z1 = m[mt][1] == -INFINITY ? 0.0f : m[mt][1];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float e0 = ex2(s[mt][n][0] - z0), e1 = ex2(s[mt][n][1] - z0);
@@ -637,7 +614,20 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
 
         // ---- the four warps' sums, through the drained ring
         cp_async_wait<0>();
-        __syncthreads();
+        if constexpr (FP8) {
+            bool huge = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) huge = huge || (fabsf(m[mt][e]) > HUGE_POINT && m[mt][e] > -INFINITY);
+            again = __syncthreads_or(huge) && !again;
+            if (again) {
+                u = u0;
+                continue;
+            }
+        } else {
+            __syncthreads();
+        }
         float* join = reinterpret_cast<float*>(ring);
         float* jm = join + S::WARPS * R * D;                   // [WARPS][R] maxima, then sums
         float* jl = jm + S::WARPS * R;
@@ -646,7 +636,15 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = mt * 16 + g + 8 * e;
-                float x = l[mt][e];
+                float x = l[mt][e], f = 1.0f;
+                if constexpr (FP8) {
+                    if (unit != 0.0f) {  // back to units of 1; where m cannot take it, the sums
+                        const bool sums = fabsf(m[mt][e]) > HUGE_POINT && m[mt][e] > -INFINITY;
+                        f = sums ? exp2_whole(unit) : 1.0f;
+                        x *= sums ? 1.0f : exp2_whole(-unit);
+                        m[mt][e] += sums ? 0.0f : unit;
+                    }
+                }
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 if (c4 == 0) {
@@ -659,8 +657,8 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                     if constexpr (FP8) {
                         // tiles 2i and 2i + 1 hold the even and odd values of 16
                         const int d = (n >> 1) * 16 + c4 * 4 + (n & 1);
-                        to[d] = acc[mt][n][2 * e];
-                        to[d + 2] = acc[mt][n][2 * e + 1];
+                        to[d] = acc[mt][n][2 * e] * f;
+                        to[d + 2] = acc[mt][n][2 * e + 1] * f;
                     } else {
                         *reinterpret_cast<float2*>(to + n * 8 + c4 * 2) =
                             make_float2(acc[mt][n][2 * e], acc[mt][n][2 * e + 1]);
@@ -703,6 +701,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                 }
             }
         }
+        unit = 0.0f;
         __syncthreads();   // the ring and the query rows are free again
     }
 }

@@ -164,9 +164,10 @@ __device__ __forceinline__ Item find_item(const AttendParams& p, long long u) {
 // 2^E4M3_HEAD (the rows kernel; the tensor-memory kernel, where a move costs
 // more, at 2).  11 bits are kept down to 2^-14 and an absolute 2^-25 below:
 // down to 2^-24 (2^-15) of the largest, and 2^-35 (2^-26) of it.  l and o are
-// in the same units.  Keys without values do not raise m, whatever their
-// scale: they add to l only, and m follows them at a distance of
-// 2^EMPTY_BELOW, where l (up to 2^26 such keys) still fits fp32.
+// in the same units.  The scale of a key without values does not raise m, and
+// on the tensor-memory kernel neither does its score: it adds to l only, and m
+// follows it at a distance of 2^EMPTY_BELOW, where l still fits fp32 (2^26
+// such keys); so it follows keys of scales below 2^-EMPTY_BELOW.
 constexpr float E4M3_HEAD = 10.0f, E4M3_LAG = 15.0f, EMPTY_BELOW = 70.0f;
 // Beside a larger m fp32 holds no such distances: the largest is then put at 1.
 constexpr float HUGE_POINT = 1048576.0f;
@@ -184,7 +185,9 @@ __device__ __forceinline__ float log2_above(float scale) {
     const int e = (int)((top + 0x007FFFFFu) >> 23) - 127;
     return (float)(e < LO ? LO : e > 100 ? 100 : e);
 }
-constexpr int LOG2_K = -100, LOG2_V = -70;    // the lowest for scales of K and of V (-EMPTY_BELOW)
+// The lowest; for the scales of a tile of V on the tensor-memory kernel as far
+// as m follows.
+constexpr int LOG2_LOW = -100, LOG2_LOW_TILE = -70;
 
 // One thread of each CTA: the record of the item that holds the first unit of
 // its run, if an earlier CTA began it and no other CTA's run begins between.
@@ -205,6 +208,32 @@ __device__ __forceinline__ void put_join(const AttendParams& p, const Item& it, 
     }
     p.join[c] = r;
 }
+
+// ------------------------------------------------------------- conversions
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 codes as two halves (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+    return r;
+}
+
+// 2^e of a whole number within [-126, 127].
+__device__ __forceinline__ float exp2_whole(float e) { return __uint_as_float((uint32_t)(127 + (int)e) << 23); }
 
 // Programmatic dependent launch: a kernel lets the next one of its call be
 // set up beside it, and waits for the one before to be complete.

@@ -51,31 +51,11 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// The same of weights that may pass the type's range: those of keys without
+// f16x2 of weights that may pass the type's range: those of keys without
 // values, which meet zeros.
 __device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
     return r;
 }
 __device__ __forceinline__ void sts16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -110,8 +90,6 @@ __device__ __forceinline__ bool group_any(int id, bool v) {
     return r != 0;
 }
 
-// 2^e of a whole number within [-100, 100].
-__device__ __forceinline__ float exp2_whole(float e) { return __uint_as_float((uint32_t)(127 + (int)e) << 23); }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -183,6 +161,25 @@ __device__ __forceinline__ void weights(const float* s, float c, float z, const 
         pk[k / 2 + 1] = FP8 ? f16x2_sat(e[2], e[3]) : bf16x2(e[2], e[3]);
     }
     tmem_st16(to, pk);
+}
+
+// Which of a lane's four token rows (those in `ask`) hold no code but 0 in the
+// D bytes of one head.  Called seldom: out of line, for the registers.
+template <int D>
+__device__ __noinline__ uint32_t keys_without_values(const uint8_t* plane, int rowb, int4 row, uint32_t ask) {
+    uint32_t none = 0;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const int r = i == 0 ? row.x : i == 1 ? row.y : i == 2 ? row.z : row.w;
+        if (!((ask >> i) & 1)) continue;
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>(plane + (size_t)r * rowb);
+        uint32_t some = 0;
+#pragma unroll 1
+        for (int d = 0; d < D / 4; ++d) some |= __ldg(codes + d);
+        if (!(some & 0x7F7F7F7Fu)) none |= 1u << i;
+    }
+    __syncwarp();
+    return none;
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
@@ -476,32 +473,29 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                         make_int4(row[0] >= 0 ? row[0] : spare, row[1] >= 0 ? row[1] : spare,
                                   row[2] >= 0 ? row[2] : spare, row[3] >= 0 ? row[3] : spare);
                 if constexpr (FP8) {
-                    // a token without values (its scale is 1, as an append
-                    // stores it): no scale, so that it takes no bits from the
-                    // tile's values and the softmax knows it
-                    float empty = 0.0f;
-                    if (__any_sync(0xffffffffu, vs[0] == 1.0f || vs[1] == 1.0f || vs[2] == 1.0f || vs[3] == 1.0f)) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll 1
-                            for (uint32_t ones = __ballot_sync(0xffffffffu, vs[i] == 1.0f); ones; ones &= ones - 1) {
-                                const int of = __ffs(ones) - 1;    // all lanes look at this one's key
-                                const size_t at = (size_t)__shfl_sync(0xffffffffu, row[i], of) * p.c.rowb + it.h * D;
-                                const uint32_t codes =
-                                    lane < D / 4 ? __ldg(reinterpret_cast<const uint32_t*>(p.c.v + at) + lane) : 0;
-                                if (!__any_sync(0xffffffffu, codes & 0x7F7F7F7Fu)) {
-                                    if (lane == of) vs[i] = 0.0f;
-                                    empty = 1.0f;
-                                }
-                            }
-                    }
                     // scales relative to the power of two at or above the
                     // tile's largest, times 2^UP: codes of up to 448 then
                     // use f16 from its top
-                    const float lk = log2_above<LOG2_K>(fmaxf(fmaxf(fabsf(ks[0]), fabsf(ks[1])),
-                                                              fmaxf(fabsf(ks[2]), fabsf(ks[3]))));
-                    const float lv = log2_above<LOG2_V>(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
-                                                              fmaxf(fabsf(vs[2]), fabsf(vs[3]))));
+                    const float lk = log2_above<LOG2_LOW>(fmaxf(fmaxf(fabsf(ks[0]), fabsf(ks[1])),
+                                                                fmaxf(fabsf(ks[2]), fabsf(ks[3]))));
+                    auto top_v = [&]() {
+                        return log2_above<LOG2_LOW_TILE>(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
+                                                        fmaxf(fabsf(vs[2]), fabsf(vs[3]))));
+                    };
+                    float lv = top_v(), empty = 0.0f;
+                    // a token without values (its scale is 1, as an append
+                    // stores it): no scale, so that it takes no bits from the
+                    // tile's values and the softmax knows it
+                    if (lv >= 0.0f) {
+                        const uint32_t none = keys_without_values<D>(
+                            p.c.v + it.h * D, p.c.rowb, make_int4(row[0], row[1], row[2], row[3]),
+                            (vs[0] == 1.0f) | (vs[1] == 1.0f) << 1 | (vs[2] == 1.0f) << 2 | (vs[3] == 1.0f) << 3);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((none >> i) & 1) vs[i] = 0.0f;
+                        empty = __any_sync(0xffffffffu, none) ? 1.0f : 0.0f;
+                        lv = top_v();
+                    }
                     const float dk = exp2_whole(UP - lk), dv = exp2_whole(UP - lv);
                     if (lane == 0) {
                         m_lk[ms] = lk - UP;
