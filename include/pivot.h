@@ -458,7 +458,7 @@ size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
  * of the tile), keeps 11 bits down to 2^-24 (2^-15) of the largest of them so
  * far, and an error of 2^-35 (2^-26) of it below.  The scale of a token
  * without values takes no part in that (more than 32 rows: a scale of 1, as an
- * append stores it), and with more than 32 rows its weight neither, up to 2^70
+ * append stores it, which tokens with values do not have), and with more than 32 rows its weight neither, up to 2^70
  * times the others', so a token of zeros may hold nearly all of the weight. */
 typedef struct {
     int32_t Hq;                  /* query heads, a multiple of Hkv               */

@@ -150,3 +150,20 @@ def test_large_values_under_a_late_large_score(size, lift, B, n, Hq, topk):
     assert float(((got[0].double() - want[0]).abs() / want[2]).max()) < 2 * 2.0 ** -8 + 2.0 ** -10
     assert float((got[1].double() - want[1]).abs().max()) < 5e-4
     assert pv.device_error() == 0
+
+
+@pytest.mark.parametrize("B,n,Hq,topk", FORMS)
+def test_one_scale_for_all_tokens(B, n, Hq, topk):
+    # a cache with scale 1 throughout, some of its tokens zero
+    gen = torch.Generator().manual_seed(24)
+    c, _ = fill([3000], 64, 1, 128, True, seed=24)
+    c.ks.fill_(0.25)
+    for plane in (c.k, c.v):
+        plane.copy_((2 * torch.randn(plane.shape, generator=gen)).to(plane.dtype))
+    empty = torch.randperm(3000, generator=gen)[:200].to(DEV)
+    page, slot = c.table[0].long()[empty // 64], empty % 64
+    c.v.view(torch.uint8)[page, slot] = 0
+    c.vs.fill_(1.0)
+    q = torch.randn(n, Hq, 128, generator=gen).to(torch.bfloat16).to(DEV)
+    picked = torch.randperm(3000 - n, generator=gen)[:2000] if topk else None
+    agree(*attend(c, q, B, 3000, picked))

@@ -164,19 +164,22 @@ __device__ __forceinline__ void weights(const float* s, float c, float z, const 
 }
 
 // Which of a lane's four token rows (those in `ask`) hold no code but 0 in the
-// D bytes of one head.  Called seldom: out of line, for the registers.
+// D bytes of one head; each is read as far as it has to be.  Called seldom: out
+// of line, for the registers.
 template <int D>
 __device__ __noinline__ uint32_t keys_without_values(const uint8_t* plane, int rowb, int4 row, uint32_t ask) {
-    uint32_t none = 0;
-#pragma unroll 1
+    const int r[4] = {row.x, row.y, row.z, row.w};
+    uint32_t c[4], none = 0;
+    auto word = [&](int i, int d) {
+        return __ldg(reinterpret_cast<const uint32_t*>(plane + (size_t)r[i] * rowb) + d) & 0x7F7F7F7Fu;
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = (ask >> i) & 1 ? word(i, 0) : 1u;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = i == 0 ? row.x : i == 1 ? row.y : i == 2 ? row.z : row.w;
-        if (!((ask >> i) & 1)) continue;
-        const uint32_t* codes = reinterpret_cast<const uint32_t*>(plane + (size_t)r * rowb);
-        uint32_t some = 0;
 #pragma unroll 1
-        for (int d = 0; d < D / 4; ++d) some |= __ldg(codes + d);
-        if (!(some & 0x7F7F7F7Fu)) none |= 1u << i;
+        for (int d = 1; d < D / 4 && c[i] == 0; ++d) c[i] = word(i, d);
+        if (c[i] == 0) none |= 1u << i;
     }
     __syncwarp();
     return none;
@@ -419,6 +422,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
             };
             auto counts = [&](int pos) { return pos >= key_lo && pos <= lim_hi; };
             int pos_a[4], page_a[4], pos_b[4];
+            bool ones = false;         // e4m3: some token with values has scale 1
             auto pages_of = [&]() {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -485,16 +489,21 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     float lv = top_v(), empty = 0.0f;
                     // a token without values (its scale is 1, as an append
                     // stores it): no scale, so that it takes no bits from the
-                    // tile's values and the softmax knows it
-                    if (lv >= 0.0f) {
-                        const uint32_t none = keys_without_values<D>(
-                            p.c.v + it.h * D, p.c.rowb, make_int4(row[0], row[1], row[2], row[3]),
-                            (vs[0] == 1.0f) | (vs[1] == 1.0f) << 1 | (vs[2] == 1.0f) << 2 | (vs[3] == 1.0f) << 3);
+                    // tile's values and the softmax knows it.  Not asked for
+                    // where tokens with values have that scale too.
+                    if (lv >= 0.0f && !ones) {
+                        const uint32_t ask =
+                            (vs[0] == 1.0f) | (vs[1] == 1.0f) << 1 | (vs[2] == 1.0f) << 2 | (vs[3] == 1.0f) << 3;
+                        if (__any_sync(0xffffffffu, ask)) {
+                            const uint32_t none = keys_without_values<D>(
+                                p.c.v + it.h * D, p.c.rowb, make_int4(row[0], row[1], row[2], row[3]), ask);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if ((none >> i) & 1) vs[i] = 0.0f;
-                        empty = __any_sync(0xffffffffu, none) ? 1.0f : 0.0f;
-                        lv = top_v();
+                            for (int i = 0; i < 4; ++i)
+                                if ((none >> i) & 1) vs[i] = 0.0f;
+                            empty = __any_sync(0xffffffffu, none) ? 1.0f : 0.0f;
+                            ones = __any_sync(0xffffffffu, ask & ~none);
+                            lv = top_v();
+                        }
                     }
                     const float dk = exp2_whole(UP - lk), dv = exp2_whole(UP - lv);
                     if (lane == 0) {
