@@ -46,8 +46,8 @@ LIB_DEBUG = os.path.join(HERE, "libpivot_debug.so")
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Build libpivot.so; with debug=True, libpivot_debug.so instead: the same
-    sources with PIVOT_DEBUG defined, so every kernel checks its own index
-    invariants and reports a failed check through the device error word
+    sources with PIVOT_DEBUG defined, so the kernels check their index
+    invariants (PIVOT_CHECK) and report a failed check through the device error word
     (pivot_get_device_error returns PIVOT_ERR_DEVICE) instead of trapping."""
     lib = LIB_DEBUG if debug else LIB
     if not force and os.path.exists(lib) and \

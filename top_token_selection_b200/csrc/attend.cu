@@ -128,9 +128,9 @@ __device__ __forceinline__ void cp4_or_zero(uint32_t dst, const void* src, bool 
 // mma.sync, not tcgen05: the loads should bound up to 32 rows a key, and
 // register fragments let each warp run alone on keys gathered from anywhere.
 // They do for bf16: a two-token step over 32 caches of 32K to 128K tokens
-// takes 760 us for 5.0 GB, 6.5 TB/s, as a plain copy reaches.  e4m3 codes
+// takes 765 us for 5.0 GB, 6.5 TB/s, as a plain copy reaches.  e4m3 codes
 // become halves first, two a conversion, and the instructions set the pace:
-// 477 us for 2.5 GB, 5.2 TB/s (536 us at a long run's clock).  Three CTAs an
+// 519 us for 2.5 GB in turn with other work, 4.8 TB/s (486 in a short run).  Three CTAs an
 // SM at 168 registers and two stages instead of two at 255 and three moved
 // the e4m3 step by 1% and the same step of one key/value head by 2% the other
 // way.

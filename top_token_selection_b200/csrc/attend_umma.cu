@@ -27,10 +27,10 @@
 // cycles with both operands in shared memory and 75 with P in TMEM (64 would
 // be the nominal rate; measured back to back), 103 when the two alternate:
 // about 3300 cycles for 256 rows x 128 keys at D = 128.  2048 new tokens over
-// 32K (bf16, 32 heads on 8) take 1090 us, 1040 TFLOP/s (1284 us in a long
-// run at the clock that the power limit leaves): a tile's softmax waits for
-// its S, which waits for its last product with V, and only two tiles fit into
-// TMEM to fill the gap.  Selected keys, 64 rows of the 128: 1.7 us a tile in
+// 32K (bf16, 32 heads on 8) take 1256 us in turn with other work, 900 TFLOP/s
+// at the clock that the power limit leaves (1070 us, 1060 TFLOP/s, in a short
+// run; e4m3: 1610): a tile's softmax waits for its S, which waits for its last
+// product with V, and only two tiles fit into TMEM to fill the gap.  Selected keys, 64 rows of the 128: 1.7 us a tile in
 // bf16 and 2.2 in e4m3, the two streams' round trips, not a unit (without the
 // copies 1.75, without the conversions 2.1; warps whose lanes hold no row
 // leaving the softmax out gained nothing), and 7 to 11 us an item to fill the
