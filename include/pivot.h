@@ -443,7 +443,8 @@ size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
  * [0, p] (-1 padding) left out; an entry named twice counts twice.  idx rows
  * are what the indexer's calls write, in either order.
  * Slots past a sequence's tokens may hold anything; the tokens' own stored
- * keys and values are finite (e4m3: scales of at most 2^100).  Rows of o and
+ * keys and values are finite (e4m3: scales of at most 2^100), and so are the
+ * scores, times log2 e, in fp32.  Rows of o and
  * lse from cu_new[B] on stay as they were.
  * Products run on the tensor cores with fp32 sums, and the softmax and its
  * sums in fp32.  The weights of the product with V are rounded: to bf16

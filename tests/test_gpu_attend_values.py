@@ -167,3 +167,20 @@ def test_one_scale_for_all_tokens(B, n, Hq, topk):
     q = torch.randn(n, Hq, 128, generator=gen).to(torch.bfloat16).to(DEV)
     picked = torch.randperm(3000 - n, generator=gen)[:2000] if topk else None
     agree(*attend(c, q, B, 3000, picked))
+
+
+@pytest.mark.parametrize("B,n,Hq,topk", FORMS)
+def test_large_scores_over_values_of_nothing(B, n, Hq, topk):
+    # no value anywhere, by scales of 0 and by codes: o is 0, the log-sum-exp as ever
+    c, gen = fill([500], 32, 1, 64, True, seed=25)
+    c.vs[c.table[0, :8].long()] = 0.0
+    for page in c.table[0, 8:16].long():
+        c.v.view(torch.uint8)[page] = 0
+    q = torch.randn(n, Hq, 64, generator=gen)
+    q[:, 1::2] *= 1e28
+    q = q.to(torch.bfloat16).to(DEV)
+    picked = torch.randperm(500 - n, generator=gen)[:300] if topk else None
+    (o, lse), want = attend(c, q, B, 500, picked)
+    assert pv.device_error() == 0 and not bool(o.any())
+    assert float((lse.double() / want[1] - 1).abs()[:, 1::2].max()) < 2 ** -16
+    assert float((lse.double() - want[1]).abs()[:, ::2].max()) < 5e-4

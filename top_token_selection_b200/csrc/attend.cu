@@ -130,10 +130,10 @@ __device__ __forceinline__ void cp4_or_zero(uint32_t dst, const void* src, bool 
 // They do for bf16: a two-token step over 32 caches of 32K to 128K tokens
 // takes 765 us for 5.0 GB, 6.5 TB/s, as a plain copy reaches.  e4m3 codes
 // become halves first, two a conversion, and the instructions set the pace:
-// 519 us for 2.5 GB in turn with other work, 4.8 TB/s (486 in a short run).  Three CTAs an
-// SM at 168 registers and two stages instead of two at 255 and three moved
-// the e4m3 step by 1% and the same step of one key/value head by 2% the other
-// way.
+// 519 us for 2.5 GB in turn with other work, 4.8 TB/s (486 in a short run).
+// Three CTAs an SM at 168 registers and two stages instead of two at 255 and
+// three moved the e4m3 step by 1% and the same step of one key/value head by
+// 2% the other way.
 template <int D, bool FP8, int MT>
 struct RowsShape {
     static constexpr int WARPS = 4;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                 const int row = page == -2 ? -1 : p.c.row_of(page, pos);
                 if (row >= 0) most = fmaxf(most, fabsf(p.c.vs[row]));
             }
-            unit = log2_above<LOG2_LOW>(most);
+            unit = __any_sync(0xffffffffu, most > 0.0f) ? log2_above<LOG2_LOW_V>(most) : 0.0f;
         }
         int pos_a = position(ta), page_a = page_of(pos_a);      // step to copy next
         int pos_b = position(ta + 1);                           // and the one after
@@ -490,9 +490,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
             // is log2 of the step's largest value scale); the sums move only
             // when it does
             float lv = 0.0f;
-            if constexpr (FP8) {
-                lv = fmaxf(log2_above<LOG2_LOW>(sc[KW + lane]), -EMPTY_BELOW);
-            }
+            if constexpr (FP8) lv = log2_above<LOG2_LOW_V>(sc[KW + lane]);
             uint32_t pf[MT][NT / 2][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -531,7 +529,7 @@ __global__ void __launch_bounds__(128, ROWS_CTAS_PER_SM) attend_rows_kernel(cons
                         if (!__all_sync(0xffffffffu, some & 0x7F7F7F7Fu)) {
                             if (!(some & 0x7F7F7F7Fu)) sc[KW + lane] = 0.0f;
                             __syncwarp();
-                            lv = fmaxf(log2_above<LOG2_LOW>(sc[KW + lane]), -EMPTY_BELOW);
+                            lv = log2_above<LOG2_LOW_V>(sc[KW + lane]);
                         }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) mx[e] += lv;

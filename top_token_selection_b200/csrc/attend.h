@@ -185,9 +185,8 @@ __device__ __forceinline__ float log2_above(float scale) {
     const int e = (int)((top + 0x007FFFFFu) >> 23) - 127;
     return (float)(e < LO ? LO : e > 100 ? 100 : e);
 }
-// The lowest; for the scales of a tile of V on the tensor-memory kernel as far
-// as m follows.
-constexpr int LOG2_LOW = -100, LOG2_LOW_TILE = -70;
+// The lowest, for scales of K; for those of V as far as m follows keys.
+constexpr int LOG2_LOW = -100, LOG2_LOW_V = -70;
 
 // One thread of each CTA: the record of the item that holds the first unit of
 // its run, if an earlier CTA began it and no other CTA's run begins between.

@@ -483,7 +483,7 @@ __global__ void __maxnreg__((UmmaShape<D, FP8, SELECTED, SPLIT>::REGS))
                     const float lk = log2_above<LOG2_LOW>(fmaxf(fmaxf(fabsf(ks[0]), fabsf(ks[1])),
                                                                 fmaxf(fabsf(ks[2]), fabsf(ks[3]))));
                     auto top_v = [&]() {
-                        return log2_above<LOG2_LOW_TILE>(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
+                        return log2_above<LOG2_LOW_V>(fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])),
                                                         fmaxf(fabsf(vs[2]), fabsf(vs[3]))));
                     };
                     float lv = top_v(), empty = 0.0f;
