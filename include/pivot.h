@@ -444,8 +444,8 @@ size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
  * are what the indexer's calls write, in either order.
  * Slots past a sequence's tokens may hold anything; the tokens' own stored
  * keys and values are finite (e4m3: scales of at most 2^100), and so are the
- * scores, times log2 e, in fp32.  Rows of o and
- * lse from cu_new[B] on stay as they were.
+ * scores, times log2 e, in fp32.  Rows of o and lse from cu_new[B] on stay as
+ * they were.
  * Products run on the tensor cores with fp32 sums, and the softmax and its
  * sums in fp32.  The weights of the product with V are rounded: to bf16
  * beside bf16 values, to f16 beside e4m3 ones.  e4m3 codes go into the
@@ -459,8 +459,9 @@ size_t pivot_pages_compact_workspace_size(const pivot_cache_t* cache);
  * of the tile), keeps 11 bits down to 2^-24 (2^-15) of the largest of them so
  * far, and an error of 2^-35 (2^-26) of it below.  The scale of a token
  * without values takes no part in that (more than 32 rows: a scale of 1, as an
- * append stores it, which tokens with values do not have), and with more than 32 rows its weight neither, up to 2^70
- * times the others', so a token of zeros may hold nearly all of the weight. */
+ * append stores it, which tokens with values do not have).  With more than 32
+ * rows its weight takes no part either, up to 2^70 times the others'.  So a
+ * token of zeros may hold nearly all of the weight. */
 typedef struct {
     int32_t Hq;                  /* query heads, a multiple of Hkv               */
     int32_t total;               /* rows of q                                    */

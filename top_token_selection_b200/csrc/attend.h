@@ -79,7 +79,9 @@ __device__ __forceinline__ long long total_units(const AttendParams& p) {
 
 // CTAs that share the units.  On the rows kernel, whose units are small, a call
 // of few units keeps to few CTAs, three units each, so that an item leaves few
-// partial sums to join.
+// partial sums to join.  One new token over 700 (32 heads on 8), with one, three
+// and eight units a CTA: 17.4, 19.5 and 23.6 us for one sequence, 27.6, 25.6 and
+// 27.6 for eight; from 3000 tokens on the same.
 __device__ __forceinline__ int run_count(const AttendParams& p, long long units) {
     const int ncta = p.ncta;
     const long long n = p.R > 32 ? units : units / 3;
